@@ -73,7 +73,9 @@ typedef void* pi_stream_t;
 
 enum pi_dtype {
   PI_BF16 = 0, /* bf16 in/out, fp32 accumulation (tcgen05 tensor cores)   */
-  PI_F32 = 1   /* fp32 in/out, fp32 FFMA arithmetic (CUDA cores)         */
+  PI_F32 = 1,  /* fp32 in/out, fp32 FFMA arithmetic (CUDA cores)         */
+  PI_E4M3 = 2  /* only as a paged cache's type: 8-bit floats, one power-  */
+               /* of-two scale per cached vector (see "Paged cache")      */
 };
 
 enum pi_status {
@@ -109,7 +111,7 @@ typedef struct pi_attn_desc {
   int32_t Hq;   /* query heads                                                */
   int32_t Hkv;  /* key/value heads; Hq % Hkv == 0                             */
   int32_t d;    /* head dimension                                             */
-  int32_t dtype;          /* enum pi_dtype                                    */
+  int32_t dtype;          /* PI_BF16 or PI_F32                                */
   float softmax_scale;    /* multiplies q.k before the softmax (finite, > 0)  */
   int64_t mask_batch_stride; /* elements between batch rows of ar_mask and
                                 segment_ids; 0 = shared by the batch, else >= Sq */
@@ -288,8 +290,9 @@ int pi_attn_debug_tiles(const pi_attn_desc* desc, const uint8_t* ar_mask,
 
 /*
  * pi_attn_read_status -- synchronises `stream`, returns the device status word
- * (PI_OK or the first PI_ERR_TIMEOUT recorded by any kernel since the last
- * read) and clears it.  Returns PI_ERR_CUDA if the synchronisation fails.
+ * (PI_OK, or the first error recorded by any kernel since the last read:
+ * PI_ERR_TIMEOUT, or PI_ERR_ARG for a length or page id that a paged call found
+ * out of range) and clears it.  Returns PI_ERR_CUDA if the synchronisation fails.
  */
 int pi_attn_read_status(pi_stream_t stream);
 
@@ -344,6 +347,121 @@ int pi_attn_suffix_noalloc(const pi_attn_desc* desc, const void* q_suf, const vo
 
 /* Size in bytes of the fixed buffer pi_attn_suffix_noalloc uses. */
 size_t pi_attn_suffix_noalloc_capacity(void);
+
+/*
+ * Paged cache -- serving many sequences of different lengths from one pool.
+ * The pages' sampler keeps one dense prefix cache per batch (1.6); these calls
+ * hold the same cached keys and values in fixed-size pages instead, so that
+ * each sequence has its own length, grows without moving, may share pages
+ * with others, and may be held in 8 bits.
+ *
+ *   k_pages, v_pages [num_pages, page_size, Hkv, d]   cache_dtype
+ *   k_exp, v_exp     [num_pages, page_size, Hkv] uint8, PI_E4M3 only (NULL
+ *                    otherwise): the vector stands for e4m3 * 2^(byte - 127)
+ *   page_table       [B, max_pages] int32: page of tokens x with
+ *                    x / page_size = column; columns past the length are not read
+ *   cache_lens       [B] int32: tokens already cached
+ *
+ * Quantisation (PI_E4M3): a vector's scale is the smallest power of two, at
+ * least 2^-126, that brings its largest magnitude to at most 448; its elements
+ * are rounded to nearest even once, at most 2^-4 of their value (down to
+ * 2^-14 of the largest; below that 2^-10 of the scale), and the scale is undone
+ * exactly.  NaN stays NaN; a vector holding an infinity reads back infinite
+ * there and flushes its finite elements.
+ *
+ * Lengths, tables and masks are device data: a length outside [0, max_pages *
+ * page_size] is clamped, a page id outside [0, num_pages) reads as zeros and
+ * is never written, and either records PI_ERR_ARG in the status word
+ * (pi_attn_read_status).  No call reads or writes outside the buffers.
+ */
+typedef struct pi_paged_desc {
+  int32_t B;            /* sequences (B == 0 is a no-op)                       */
+  int32_t Sq;           /* tokens per sequence: new tokens, or rows to read     */
+  int32_t Hq;           /* query heads (pi_attn_paged only)                    */
+  int32_t Hkv;          /* key/value heads; Hq % Hkv == 0                      */
+  int32_t d;            /* head dimension: 32, 64, 128 or 256                  */
+  int32_t dtype;        /* of the dense tensors: PI_BF16 or PI_F32             */
+  int32_t cache_dtype;  /* of the pools: dtype or PI_E4M3                      */
+  int32_t page_size;    /* tokens per page: 16, 32, 64, 128 or 256             */
+  int32_t num_pages;    /* pages in the pool                                   */
+  int32_t max_pages;    /* columns of page_table                               */
+  int32_t window;       /* pi_attn_paged: 0 = none, else see there             */
+  int32_t sinks;        /* pi_attn_paged: first tokens that stay visible       */
+  float softmax_scale;  /* pi_attn_paged: multiplies q.k (finite, > 0)         */
+  int32_t reserved;     /* 0                                                   */
+  int64_t mask_batch_stride; /* token_mask / ar_mask / segment_ids: 0 = shared
+                                by the batch, else >= Sq                       */
+} pi_paged_desc;
+
+/*
+ * pi_attn_cache_write -- appends Sq new tokens of every sequence to the cache.
+ *   k_new, v_new [B, Sq, Hkv, d]  dtype
+ *   token_mask   [B or 1, Sq] uint8 or NULL (all valid): only valid tokens are
+ *                stored, packed: token t goes to position cache_lens[b] + (valid
+ *                tokens before t), the position pi_rope_inplace gives it
+ *   lens_out     [B] int32 or NULL: the lengths after the call.  May not be
+ *                cache_lens itself (PI_ERR_ARG); written also when Sq == 0
+ * Tokens past the page table's room are not stored (PI_ERR_ARG in the status
+ * word).  Everything outside the written slots is left as it was.  A page that is written must
+ * belong to one sequence of the call.  desc: Hq, window, sinks and
+ * softmax_scale are not read; Sq <= 16383.
+ */
+int pi_attn_cache_write(const pi_paged_desc* desc, const void* k_new, const void* v_new,
+                        const uint8_t* token_mask, const int32_t* page_table,
+                        const int32_t* cache_lens, void* k_pages, void* v_pages, uint8_t* k_exp,
+                        uint8_t* v_exp, int32_t* lens_out, pi_stream_t stream);
+
+/*
+ * pi_attn_cache_read -- rows [0, Sq) of every sequence as dense tensors, ready
+ * for the dense entry points (pi_attn_suffix_masked's k_cache, v_cache and
+ * cache_valid).
+ *   k_out, v_out [B, Sq, Hkv, d] dtype: the cached vectors (rounded to dtype
+ *                once); rows past a sequence's length are zeros
+ *   valid_out    [B, Sq] uint8 or NULL: 1 for a cached row, 0 past the length
+ * desc: as pi_attn_cache_write; mask_batch_stride is not read; any Sq.
+ */
+int pi_attn_cache_read(const pi_paged_desc* desc, const void* k_pages, const void* v_pages,
+                       const uint8_t* k_exp, const uint8_t* v_exp, const int32_t* page_table,
+                       const int32_t* cache_lens, void* k_out, void* v_out, uint8_t* valid_out,
+                       pi_stream_t stream);
+
+/*
+ * pi_attn_paged -- attention of a chunk of new tokens over the paged cache:
+ * pi_attn_suffix_masked with every sequence's own length.  One new token
+ * (Sq == 1) is a decoding step.
+ *   q            [B, Sq, Hq, d];  k_new, v_new [B, Sq, Hkv, d]
+ *   ar_mask      [B or 1, Sq] uint8 (all nonzero: causal among the new tokens)
+ *   segment_ids  [B or 1, Sq] int32 or NULL, as in pi_attn_suffix_masked
+ *   out          [B, Sq, Hq, d]; lse [B, Sq, Hq] fp32 or NULL (natural log)
+ * Query i of sequence b sees the cached keys [0, cache_lens[b]) and the new
+ * keys by the block-index rule.  The new tokens need not be in the cache: the
+ * call reads positions below cache_lens only, so it may run before or after
+ * pi_attn_cache_write stores them (with the lengths from before).
+ * With window > 0, a key at position x is hidden from query i, which stands at
+ * position cache_lens[b] + i, unless cache_lens[b] + i - x < window or
+ * x < sinks; new key j stands at position cache_lens[b] + j (padding tokens
+ * count, so the positions are the stored ones when padding is on the right).
+ * window == 0: no limit (sinks is not read).
+ * A row that sees no key writes out = 0, lse = -inf.  What masked or stale
+ * slots hold (NaN included) does not reach the result, except that a
+ * non-finite value vector seen by some query of a sequence may make the
+ * sequence's other rows non-finite too.
+ *   workspace    device scratch of pi_attn_paged_workspace_bytes(desc) bytes,
+ *                16-byte aligned, contents ignored (NULL when that is 0);
+ *                calls that may overlap need distinct workspaces
+ * Supported: Sq <= 16383, B <= 65535, num_pages * page_size and max_pages *
+ * page_size below 2^31 - 2^15.  Runs on tensor cores: bf16, d == 256, Hq / Hkv
+ * in {1, 2, 4, 8, 16}; everything else on CUDA cores (fp32 arithmetic).
+ * Errors (all three calls): PI_ERR_ARG, PI_ERR_ALIGN (dense tensors, pools and
+ * workspace 16 bytes; int32 and fp32 arrays 4), PI_ERR_UNSUPPORTED before
+ * anything is enqueued; PI_ERR_CUDA if a launch fails.
+ */
+size_t pi_attn_paged_workspace_bytes(const pi_paged_desc* desc);
+int pi_attn_paged(const pi_paged_desc* desc, const void* q, const void* k_new, const void* v_new,
+                  const uint8_t* ar_mask, const int32_t* segment_ids, const void* k_pages,
+                  const void* v_pages, const uint8_t* k_exp, const uint8_t* v_exp,
+                  const int32_t* page_table, const int32_t* cache_lens, void* out, float* lse,
+                  void* workspace, size_t ws_bytes, pi_stream_t stream);
 
 /*
  * Steps on either side of the attention (the Euler sampling loop of

@@ -33,6 +33,9 @@ Parity status per function (what pins it; tests live in tests/test_oracle.py):
   positions example with padding and a padded prefix, RoPE's closed forms
   (identity at 0, pair norms kept, a stated turn of pairs 0 and 4), the
   relative-position property, and the Euler loop against the exact solution.
+* ``paged`` -- pinned: the e4m3 grid against torch's float8_e4m3fn (every bit
+  pattern and rounding), the exponent's defining inequality, and ``attend``
+  against ``attention.suffix`` (dense caches, padding) and a windowed mask.
 * ``counts.full_pairs`` / ``visible_pairs`` -- pinned: the pages' worked
   counts (480^2 = 230,400 fused scores, 32 x 448 cross scores, 28 x 4250^2
   MM-DiT pairs) and the number of True entries of the explicit masks.
@@ -50,4 +53,4 @@ from .attention import (  # noqa: F401
     suffix,
     suffix_mask,
 )
-from . import backward, brute, counts, prepost  # noqa: F401
+from . import backward, brute, counts, paged, prepost  # noqa: F401

@@ -8,11 +8,13 @@ library cannot be loaded, every call raises.
 
 Names mirror the C ABI in include/pi_attn.h: ``pi_attn_prefill``,
 ``pi_attn_suffix``, ``pi_attn_suffix_workspace_bytes``, ``pi_attn_debug_mask``,
-``pi_attn_read_status``, ``pi_attn_set_wait_limit``, ``pi_attn_selftest_wait``.
+``pi_attn_read_status``, ``pi_attn_set_wait_limit``, ``pi_attn_selftest_wait``,
+``pi_attn_cache_write``, ``pi_attn_cache_read``, ``pi_attn_paged``.
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -20,7 +22,7 @@ import torch
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpiattn.so")
 
-PI_BF16, PI_F32 = 0, 1
+PI_BF16, PI_F32, PI_E4M3 = 0, 1, 2
 PI_OK, PI_ERR_ARG, PI_ERR_ALIGN, PI_ERR_UNSUPPORTED, PI_ERR_CUDA, PI_ERR_TIMEOUT = range(6)
 
 EXPORTED = (
@@ -43,6 +45,10 @@ EXPORTED = (
     "pi_attn_prefill_ws",
     "pi_attn_prefill_workspace_bytes",
     "pi_attn_prefill_tail_splits",
+    "pi_attn_cache_write",
+    "pi_attn_cache_read",
+    "pi_attn_paged",
+    "pi_attn_paged_workspace_bytes",
 )
 
 
@@ -77,6 +83,26 @@ class PiAttnDesc(ctypes.Structure):
         ("d", ctypes.c_int32),
         ("dtype", ctypes.c_int32),
         ("softmax_scale", ctypes.c_float),
+        ("mask_batch_stride", ctypes.c_int64),
+    ]
+
+
+class PiPagedDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32),
+        ("Sq", ctypes.c_int32),
+        ("Hq", ctypes.c_int32),
+        ("Hkv", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("cache_dtype", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("sinks", ctypes.c_int32),
+        ("softmax_scale", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
         ("mask_batch_stride", ctypes.c_int64),
     ]
 
@@ -132,6 +158,15 @@ def lib() -> ctypes.CDLL:
         L.pi_attn_prefill_backward.restype = i32
         L.pi_attn_suffix_noalloc_capacity.argtypes = []
         L.pi_attn_suffix_noalloc_capacity.restype = sz
+        pp = ctypes.POINTER(PiPagedDesc)
+        L.pi_attn_cache_write.argtypes = [pp] + [vp] * 11
+        L.pi_attn_cache_write.restype = i32
+        L.pi_attn_cache_read.argtypes = [pp] + [vp] * 10
+        L.pi_attn_cache_read.restype = i32
+        L.pi_attn_paged_workspace_bytes.argtypes = [pp]
+        L.pi_attn_paged_workspace_bytes.restype = sz
+        L.pi_attn_paged.argtypes = [pp] + [vp] * 14 + [sz, vp]
+        L.pi_attn_paged.restype = i32
         _lib = L
     return _lib
 
@@ -420,6 +455,191 @@ def pi_euler_update(x, v, dt, stream=None):
     if rc != PI_OK:
         raise PiAttnError(rc, "pi_euler_update")
     return x
+
+
+# ------------------------------------------------------------- paged cache
+
+_CACHE_CODES = {torch.bfloat16: PI_BF16, torch.float32: PI_F32, torch.float8_e4m3fn: PI_E4M3}
+
+
+def _paged_desc(B, Sq, Hq, dtype, k_pages, v_pages, page_table, cache_lens, k_exp, v_exp,
+                window=0, sinks=0, softmax_scale=1.0, mask_stride=0):
+    """Checks the cache's tensors against each other and returns the descriptor."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"unsupported dtype {dtype}")
+    _need(k_pages, "k_pages", dims=4)
+    _need(v_pages, "v_pages", k_pages.dtype, 4)
+    _need(page_table, "page_table", torch.int32, 2)
+    _need(cache_lens, "cache_lens", torch.int32, 1)
+    if k_pages.dtype not in _CACHE_CODES:
+        raise ValueError(f"unsupported cache dtype {k_pages.dtype}")
+    shape = k_pages.shape
+    if v_pages.shape != shape:
+        raise ValueError("v_pages must have k_pages' shape")
+    if page_table.shape[0] != B or cache_lens.shape[0] != B:
+        raise ValueError("page_table must be [B, max_pages] and cache_lens [B]")
+    if k_pages.dtype == torch.float8_e4m3fn:
+        _need(k_exp, "k_exp", torch.uint8, 3)
+        _need(v_exp, "v_exp", torch.uint8, 3)
+        if k_exp.shape != shape[:3] or v_exp.shape != shape[:3]:
+            raise ValueError("k_exp/v_exp must be [num_pages, page_size, Hkv]")
+    elif k_exp is not None or v_exp is not None:
+        raise ValueError("k_exp/v_exp belong to a float8_e4m3fn cache")
+    return PiPagedDesc(B, Sq, Hq, shape[2], shape[3],
+                       PI_BF16 if dtype == torch.bfloat16 else PI_F32,
+                       _CACHE_CODES[k_pages.dtype], shape[1], shape[0], page_table.shape[1],
+                       int(window), int(sinks), float(softmax_scale), 0, mask_stride)
+
+
+def _one_device(*tensors):
+    """The tensors' device; they must share it and it must be the current one
+    (kernels are launched there)."""
+    index = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != index:
+            raise ValueError(f"tensors must be on the current device, cuda:{index}; "
+                             f"got one on {t.device}")
+
+
+def _on(stream):
+    """A context in which tensors are allocated for use on ``stream``."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def pi_attn_cache_write(k_new, v_new, k_pages, v_pages, page_table, cache_lens, token_mask=None,
+                        k_exp=None, v_exp=None, lens_out=None, stream=None):
+    """Appends new tokens to a paged cache.  k_new, v_new [B,Sq,Hkv,d]; pools
+    [num_pages,page_size,Hkv,d] of the same dtype or float8_e4m3fn (then with
+    uint8 exponents k_exp, v_exp [num_pages,page_size,Hkv]); page_table int32
+    [B,max_pages]; cache_lens int32 [B].  Valid tokens (``token_mask`` uint8
+    [Sq] or [B,Sq], None = all) go to the positions after cache_lens, packed.
+    ``lens_out`` (int32 [B], not cache_lens) receives the new lengths."""
+    _need(k_new, "k_new", dims=4)
+    _need(v_new, "v_new", k_new.dtype, 4)
+    B, Sq, Hkv, d = k_new.shape
+    if v_new.shape != k_new.shape or tuple(k_pages.shape[2:]) != (Hkv, d):
+        raise ValueError("k_new/v_new must be [B, Sq, Hkv, d] with the pools' heads")
+    mbs = 0
+    if token_mask is not None:
+        _need(token_mask, "token_mask", torch.uint8)
+        mbs = _mask_stride(token_mask, B, Sq)
+    if lens_out is not None:
+        _need(lens_out, "lens_out", torch.int32, 1)
+        if lens_out.shape[0] != B:
+            raise ValueError("lens_out must be [B]")
+    desc = _paged_desc(B, Sq, Hkv, k_new.dtype, k_pages, v_pages, page_table, cache_lens, k_exp,
+                       v_exp, mask_stride=mbs)
+    _one_device(k_new, v_new, k_pages, v_pages, page_table, cache_lens, token_mask, k_exp, v_exp,
+                lens_out)
+    rc = lib().pi_attn_cache_write(
+        ctypes.byref(desc), _ptr(k_new), _ptr(v_new), _ptr(token_mask), _ptr(page_table),
+        _ptr(cache_lens), _ptr(k_pages), _ptr(v_pages), _ptr(k_exp), _ptr(v_exp), _ptr(lens_out),
+        ctypes.c_void_p(_stream(stream)))
+    if rc != PI_OK:
+        raise PiAttnError(rc, "pi_attn_cache_write")
+    return lens_out
+
+
+def pi_attn_cache_read(k_pages, v_pages, page_table, cache_lens, S, dtype=torch.bfloat16,
+                       k_exp=None, v_exp=None, k_out=None, v_out=None, valid_out=None,
+                       stream=None):
+    """Rows [0, S) of every sequence of a paged cache as dense [B,S,Hkv,d]
+    tensors of ``dtype`` (zeros past the length), and uint8 [B,S] validity, as
+    pi_attn_suffix takes them (``k_cache``, ``v_cache``, ``cache_valid``).
+    Returns (k, v, valid), allocated where not given."""
+    B, S = cache_lens.shape[0], int(S)
+    desc = _paged_desc(B, S, k_pages.shape[2], dtype, k_pages, v_pages, page_table, cache_lens,
+                       k_exp, v_exp)
+    shape = (B, S, *k_pages.shape[2:])
+    with _on(stream):
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=dtype, device=k_pages.device)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=dtype, device=k_pages.device)
+        if valid_out is None:
+            valid_out = torch.empty((B, S), dtype=torch.uint8, device=k_pages.device)
+    _need(k_out, "k_out", dtype, 4)
+    _need(v_out, "v_out", dtype, 4)
+    _need(valid_out, "valid_out", torch.uint8, 2)
+    if k_out.shape != shape or v_out.shape != shape or valid_out.shape != shape[:2]:
+        raise ValueError("k_out/v_out must be [B, S, Hkv, d] and valid_out [B, S]")
+    _one_device(k_pages, v_pages, page_table, cache_lens, k_exp, v_exp, k_out, v_out, valid_out)
+    rc = lib().pi_attn_cache_read(
+        ctypes.byref(desc), _ptr(k_pages), _ptr(v_pages), _ptr(k_exp), _ptr(v_exp),
+        _ptr(page_table), _ptr(cache_lens), _ptr(k_out), _ptr(v_out), _ptr(valid_out),
+        ctypes.c_void_p(_stream(stream)))
+    if rc != PI_OK:
+        raise PiAttnError(rc, "pi_attn_cache_read")
+    return k_out, v_out, valid_out
+
+
+def pi_attn_paged_workspace_bytes(q, k_new, k_pages, v_pages, page_table, cache_lens,
+                                  k_exp=None, v_exp=None, window=0, sinks=0):
+    """Bytes of workspace pi_attn_paged needs for these tensors (0 if none)."""
+    B, Sq, Hq, _ = q.shape
+    desc = _paged_desc(B, Sq, Hq, q.dtype, k_pages, v_pages, page_table, cache_lens, k_exp, v_exp,
+                       window, sinks)
+    return int(lib().pi_attn_paged_workspace_bytes(ctypes.byref(desc)))
+
+
+def pi_attn_paged(q, k_new, v_new, k_pages, v_pages, page_table, cache_lens, ar_mask,
+                  segment_ids=None, k_exp=None, v_exp=None, out=None, lse=None, workspace=None,
+                  softmax_scale=1.0, window=0, sinks=0, stream=None):
+    """Attention of a chunk of new tokens over a paged cache.  q [B,Sq,Hq,d];
+    k_new, v_new [B,Sq,Hkv,d]; the cache as in pi_attn_cache_write; ar_mask uint8
+    [Sq] or [B,Sq] and segment_ids (int32, same layout; negative = padding)
+    among the new tokens, as in pi_attn_suffix.  Every query sees its sequence's
+    first cache_lens cached keys; with ``window`` > 0 only keys less than
+    ``window`` positions back and the first ``sinks`` positions.  ``lse`` fp32
+    [B,Sq,Hq] receives the log-sum-exp.  ``workspace``: a CUDA uint8 tensor of
+    pi_attn_paged_workspace_bytes bytes (allocated here if None and needed).
+    Returns ``out`` (allocated if None)."""
+    _need(q, "q", dims=4)
+    _need(k_new, "k_new", q.dtype, 4)
+    _need(v_new, "v_new", q.dtype, 4)
+    _need(ar_mask, "ar_mask", torch.uint8)
+    B, Sq, Hq, d = q.shape
+    shape = (B, Sq, k_pages.shape[2], d)
+    if k_new.shape != shape or v_new.shape != shape or k_pages.shape[3] != d:
+        raise ValueError("k_new/v_new must be [B, Sq, Hkv, d] with the pools' heads and q's d")
+    mbs = _mask_stride(ar_mask, B, Sq)
+    if segment_ids is not None:
+        _need(segment_ids, "segment_ids", torch.int32)
+        if segment_ids.shape != ar_mask.shape:
+            raise ValueError("segment_ids must have the layout of ar_mask")
+    if lse is not None:
+        _need(lse, "lse", torch.float32, 3)
+        if lse.shape != q.shape[:3]:
+            raise ValueError("lse must be [B, Sq, Hq]")
+    desc = _paged_desc(B, Sq, Hq, q.dtype, k_pages, v_pages, page_table, cache_lens, k_exp, v_exp,
+                       window, sinks, softmax_scale, mbs)
+    need = int(lib().pi_attn_paged_workspace_bytes(ctypes.byref(desc)))
+    if out is None or (workspace is None and need > 0):
+        with _on(stream):
+            if out is None:
+                out = torch.empty_like(q)
+            if workspace is None and need > 0:
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _need(out, "out", q.dtype, 4)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8)
+    _one_device(q, k_new, v_new, k_pages, v_pages, page_table, cache_lens, ar_mask, segment_ids,
+                k_exp, v_exp, out, lse, workspace)
+    ws_bytes = 0 if workspace is None else workspace.numel()
+    rc = lib().pi_attn_paged(
+        ctypes.byref(desc), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(ar_mask), _ptr(segment_ids),
+        _ptr(k_pages), _ptr(v_pages), _ptr(k_exp), _ptr(v_exp), _ptr(page_table),
+        _ptr(cache_lens), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
+        ctypes.c_void_p(_stream(stream)))
+    if rc != PI_OK:
+        raise PiAttnError(rc, "pi_attn_paged")
+    return out
 
 
 def pi_attn_debug_mask(ar_mask, segment_ids=None, B=None, P=0, mode=0, stream=None):

@@ -4,7 +4,6 @@
 //
 // Validation happens entirely on the host, before anything is enqueued: an
 // entry point that returns an error has launched nothing.
-#include <cudaTypedefs.h>
 #include <nvtx3/nvToolsExt.h>
 
 #include <atomic>
@@ -54,6 +53,10 @@ int* status_ptr() {
   return cudaGetSymbolAddress(&p, g_status) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
+}  // namespace
+
+namespace piattn {
+
 bool make_ctl(DevCtl* ctl) {
   ctl->status = status_ptr();
   ctl->wait_limit = g_wait_limit.load();
@@ -72,6 +75,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   }();
   return fn;
 }
+
+}  // namespace piattn
+
+namespace {
 
 // A [batch][rows][256] bf16 tensor viewed as 4-D (64, rows, 4, batch): the
 // row stride is 512 B and dimension 2 walks the four 64-column blocks of a

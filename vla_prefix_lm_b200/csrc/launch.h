@@ -1,12 +1,19 @@
 // launch.h -- internal launchers behind the C ABI (host side, not exported).
 #pragma once
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
 #include "common.cuh"
 
 namespace piattn {
+
+// The device status word and the wait bound, for a launch on the current
+// device; false when the status word cannot be found (abi.cu).
+bool make_ctl(DevCtl* ctl);
+// The driver's tensor-map encoder, null if it cannot be found (abi.cu).
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 
 // Launches `kernel` so that it may begin while the previous kernel in `st` is
 // still running (programmatic stream serialization): the kernel must call

@@ -1,0 +1,119 @@
+// paged.cuh -- what the paged-cache kernels share: parameters, the e4m3
+// conversions, and the rules that turn cached lengths, the page table and the
+// sliding window into slots and visible key ranges.
+#pragma once
+#include <cstdint>
+
+#include "common.cuh"
+#include "mask.cuh"
+
+namespace piattn {
+
+constexpr int kStatusArg = 1;        // device-side: a bad length or page id
+
+constexpr int kCacheBF16 = 0, kCacheF32 = 1, kCacheE4M3 = 2;   // enum pi_dtype
+
+struct E4M3 { uint8_t bits; };
+
+// Two e4m3 values (low byte first) as floats; every e4m3 value is exact in fp16.
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint16_t v) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(v));
+  return h;
+}
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t v) {
+  const uint32_t h = e4m3x2_to_half2(v);
+  float2 f;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+      "cvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(h));
+  return f;
+}
+// lo, hi rounded to nearest e4m3 (ties to even, saturating at 448, NaN kept).
+__device__ __forceinline__ uint16_t float2_to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 2^(byte - 127): exact; byte 0 is 2^-127 (subnormal).
+__device__ __forceinline__ float exp_scale(uint32_t byte) {
+  return byte == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
+}
+
+// Writing to and reading from the pages (cache.cu).
+constexpr int kCacheMaxTok = 128;    // tokens per CTA at most
+struct CacheParams {
+  const void* k_in;                  // write: new tokens [B, S, Hkv, d]
+  const void* v_in;
+  void* k_out;                       // read: rows [B, S, Hkv, d]
+  void* v_out;
+  void* kp;                          // pools [num_pages, page, Hkv, d]
+  void* vp;
+  uint8_t* ke;                       // e4m3 pools: exponent bytes [num_pages, page, Hkv]
+  uint8_t* ve;
+  const int32_t* table;              // [B, max_pages]
+  const int32_t* lens;               // [B]
+  const uint8_t* tmask;              // write: [B or 1, S], null = all valid
+  long long tmask_bs;
+  int32_t* lens_out;                 // write: [B], may be null
+  uint8_t* valid_out;                // read: [B, S], may be null
+  int B, S, Hkv, d;
+  int page_shift, num_pages, max_pages;
+};
+cudaError_t launch_cache(const CacheParams& p, bool write, bool f32, int cache_dtype,
+                         const DevCtl& ctl, cudaStream_t st);
+
+// Attention of a chunk of new tokens over the pages.
+struct PagedParams {
+  const void* q;                     // [B, Sq, Hq, d]
+  const void* k;                     // the chunk's keys and values [B, Sq, Hkv, d]
+  const void* v;
+  const void* kp;                    // pools and exponents as in CacheParams
+  const void* vp;
+  const uint8_t* ke;
+  const uint8_t* ve;
+  const int32_t* table;
+  const int32_t* lens;
+  const uint8_t* ar;                 // chunk mask rows, segment ids (may be null)
+  const int32_t* seg;
+  long long mask_bs;
+  void* out;
+  float* lse;                        // [B, Sq, Hq], may be null
+  int B, Sq, Hq, Hkv, d;
+  int page_shift, num_pages, max_pages;
+  int window, sinks;                 // window 0: none
+  int cache_dtype;
+  bool f32;                          // q, k, v, out
+  float scale;
+};
+
+// A sequence's cached length, clamped to what its page-table row can hold.
+// `bad` is set when it had to be.
+__device__ __forceinline__ int cached_len(const int32_t* lens, int b, int max_pages,
+                                          int page_shift, bool& bad) {
+  const long long cap = (long long)max_pages << page_shift;
+  const int n = lens[b];
+  bad = bad || n < 0 || n > cap;
+  return (int)min((long long)max(n, 0), cap);
+}
+
+// Query i of a chunk stands at position len + i.  Cached keys it sees are
+// [0, sink_end) and [lo, len): everything without a window; with one, keys
+// less than `window` positions back plus the first `sinks`.
+struct CachedRange { int sink_end, lo; };
+__device__ __forceinline__ CachedRange cached_range(int len, int i, int window, int sinks) {
+  if (window <= 0) return {0, 0};
+  const int lo = min(max(len + i - window + 1, 0), len);
+  return {min(sinks, lo), lo};
+}
+
+// Whether the window lets query i see the chunk's key j.
+__device__ __forceinline__ bool in_window(int len, int i, int j, int window, int sinks) {
+  return window <= 0 || i - j < window || len + j < sinks;
+}
+
+cudaError_t launch_paged_simt(const PagedParams& p, const DevCtl& ctl, cudaStream_t st);
+
+}  // namespace piattn
