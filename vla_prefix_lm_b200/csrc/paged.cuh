@@ -109,10 +109,38 @@ __device__ __forceinline__ CachedRange cached_range(int len, int i, int window, 
   return {min(sinks, lo), lo};
 }
 
+// The n low bits set (n <= 0: none, n >= 32: all).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n >= 32 ? ~0u : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
 // Whether the window lets query i see the chunk's key j.
 __device__ __forceinline__ bool in_window(int len, int i, int j, int window, int sinks) {
   return window <= 0 || i - j < window || len + j < sinks;
 }
+
+// bf16 queries, d = 256, G = Hq / Hkv in {1, 2, 4, 8, 16} on tcgen05
+// (paged_tc.cu).  Sequences are scheduled in groups of kPagedTcGroup.
+constexpr int kPagedTcGroup = 192;
+struct PagedTcParams : PagedParams {
+  float* ws;                 // partials [n_clusters * 2][256 rows][256], then (m, l)
+  int G, tok_per_tile;       // heads per kv head; new tokens per 256-row tile
+  int n_tiles;               // query tiles per (sequence, kv head)
+  int b0, nb;                // this launch's sequences
+  int n_clusters;
+  int may_cut;               // units may be cut (ws is given)
+  int smem_bytes;
+  float scale_log2;
+};
+bool paged_tc_applies(const PagedParams& p);
+size_t paged_tc_workspace_bytes(const PagedParams& p);
+cudaError_t launch_paged_tc(const PagedParams& p, float* ws, const DevCtl& ctl, cudaStream_t st);
 
 cudaError_t launch_paged_simt(const PagedParams& p, const DevCtl& ctl, cudaStream_t st);
 

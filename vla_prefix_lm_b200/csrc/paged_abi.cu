@@ -92,6 +92,24 @@ CacheParams cache_params(const pi_paged_desc* d) {
   return p;
 }
 
+PagedParams paged_params(const pi_paged_desc* d) {
+  PagedParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.mask_bs = d->mask_batch_stride;
+  p.B = d->B; p.Sq = d->Sq; p.Hq = d->Hq; p.Hkv = d->Hkv; p.d = d->d;
+  p.page_shift = page_shift(d);
+  p.num_pages = d->num_pages;
+  p.max_pages = d->max_pages;
+  // A window that reaches back over any sequence hides nothing.  (What is
+  // left keeps every position difference inside 32 bits.)
+  p.window = (long long)d->window >= (long long)d->max_pages * d->page_size + d->Sq ? 0 : d->window;
+  p.sinks = p.window > 0 ? d->sinks : 0;
+  p.cache_dtype = d->cache_dtype;
+  p.f32 = d->dtype == PI_F32;
+  p.scale = d->softmax_scale;
+  return p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -152,8 +170,9 @@ int pi_attn_cache_read(const pi_paged_desc* d, const void* k_pages, const void* 
 }
 
 size_t pi_attn_paged_workspace_bytes(const pi_paged_desc* d) {
-  (void)d;
-  return 0;
+  if (check_attn(d) != PI_OK || d->B == 0 || d->Sq == 0) return 0;
+  const PagedParams p = paged_params(d);
+  return paged_tc_applies(p) ? paged_tc_workspace_bytes(p) : 0;
 }
 
 int pi_attn_paged(const pi_paged_desc* d, const void* q, const void* k_new, const void* v_new,
@@ -178,23 +197,16 @@ int pi_attn_paged(const pi_paged_desc* d, const void* q, const void* k_new, cons
   }
   DevCtl ctl;
   if (!make_ctl(&ctl)) return PI_ERR_CUDA;
-  PagedParams p;
-  std::memset(&p, 0, sizeof(p));
+  PagedParams p = paged_params(d);
   p.q = q; p.k = k_new; p.v = v_new;
   p.kp = k_pages; p.vp = v_pages; p.ke = k_exp; p.ve = v_exp;
   p.table = page_table; p.lens = cache_lens;
-  p.ar = ar_mask; p.seg = segment_ids; p.mask_bs = d->mask_batch_stride;
+  p.ar = ar_mask; p.seg = segment_ids;
   p.out = out; p.lse = lse;
-  p.B = d->B; p.Sq = d->Sq; p.Hq = d->Hq; p.Hkv = d->Hkv; p.d = d->d;
-  p.page_shift = page_shift(d);
-  p.num_pages = d->num_pages;
-  p.max_pages = d->max_pages;
-  p.window = d->window;
-  p.sinks = d->sinks;
-  p.cache_dtype = d->cache_dtype;
-  p.f32 = d->dtype == PI_F32;
-  p.scale = d->softmax_scale;
-  return launched(launch_paged_simt(p, ctl, static_cast<cudaStream_t>(stream)));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (paged_tc_applies(p))
+    return launched(launch_paged_tc(p, need > 0 ? static_cast<float*>(workspace) : nullptr, ctl, st));
+  return launched(launch_paged_simt(p, ctl, st));
 }
 
 }  // extern "C"
