@@ -397,15 +397,45 @@ def test_write_special_values():
         vals, byte = P.quantise(_np(x[0, t, 0]))
         assert exps[at] == byte, t
         assert np.array_equal(flat[at], vals), t
-    nan_at, inf_at = (P.slot(c.table_np, 0, t, 32) for t in (8, 9))
-    ref = _np(x[0, 8, 0])
-    ref[3] = 0
-    vals, byte = P.quantise(ref)
-    assert exps[nan_at] == byte and np.isnan(flat[nan_at][3])
-    assert np.array_equal(np.delete(flat[nan_at], 3), np.delete(vals, 3))
+    assert exps[P.slot(c.table_np, 0, 8, 32)] == 255
     c.lens += 12
     k, _, _ = b.pi_attn_cache_read(*c.args(), 12, dtype=F32, **c.exps())
+    assert torch.isnan(k[0, 8]).all()
     assert k[0, 9, 0, 3] == float("inf") and (k[0, 9, 0, 4:] == 0).all()
+
+
+@pytest.mark.parametrize("Sq", [1, 2, 5, 40])
+def test_cached_values_come_through_exactly(Sq):
+    """One visible cached key: its probability is 1 and out is its value vector,
+    rounded to bf16 only.  Every e4m3 byte and exponents over the range."""
+    b = _b()
+    c = Cache(24, [32], 32, 1, 256, E4M3)
+    bits = torch.arange(256, dtype=torch.uint8)
+    bits[0x7F] = bits[0xFF] = 0
+    slot = P.slot(c.table_np, 0, 0, 32)
+    c.v.view(torch.uint8).view(-1, 256)[slot] = bits.cuda()
+    q = _rand(c.rng, (1, Sq, 8, 256), BF16, 0.25)
+    kn = _rand(c.rng, (1, Sq, 1, 256), BF16, 0.25)
+    vn = _rand(c.rng, (1, Sq, 1, 256), BF16, 0.25)
+    seg = torch.full((Sq,), -1, dtype=torch.int32, device="cuda")
+    seg[-1] = 0
+    # the last token sees cached key 0 (a sink) and itself; its own key is far
+    # below (its score is -2^9 at least), so that its probability underflows
+    q[:] = 4.0
+    kn[:] = -4.0
+    c.k.view(torch.uint8).view(-1, 256)[slot] = 0x38           # 1.0
+    c.k_exp.view(-1)[slot] = 127
+    ar = torch.ones(Sq, dtype=torch.uint8, device="cuda")
+    for byte in list(range(0, 250, 7)) + [120, 127, 134, 135, 136, 246, 247]:
+        c.v_exp.view(-1)[slot] = byte
+        out = b.pi_attn_paged(q, kn, vn, *c.args(), ar, segment_ids=seg, window=1, sinks=1,
+                              **c.exps())
+        want = bits.view(torch.float8_e4m3fn).double() * 2.0 ** (byte - 127)
+        want = want.to(BF16).cuda()
+        tiny = want.abs().double() < 2.0 ** -126                # bf16 subnormals may be flushed
+        got = out[0, -1]
+        ok = (got == want) | (tiny & (got.abs().double() < 2.0 ** -126))
+        assert ok.all(), byte
 
 
 def test_write_past_the_room_is_dropped_and_reported():

@@ -10,7 +10,8 @@
 // so every element down to amax * 2^-14 is rounded once, by at most half a
 // step (2^-4 of it), and undoing the scale is exact in bf16 and fp32, which
 // lets the attention kernels rebuild bf16 operands without a second rounding.
-// Non-finite input: NaN stays NaN; an infinity reads back infinite (448 *
+// Non-finite input: a NaN makes the whole vector NaN (byte 255, so that no
+// reader has to look for NaN bytes); an infinity reads back infinite (448 *
 // 2^120 overflows) and flushes the finite rest of its vector.
 //
 // Both kernels move each byte once and are bound by HBM (long calls) or by
@@ -81,12 +82,19 @@ __device__ __forceinline__ void store8(E4M3* p, const F8& f) {
 template <typename T> constexpr bool kIsE4M3 = false;
 template <> constexpr bool kIsE4M3<E4M3> = true;
 
-// The exponent byte of a vector with largest finite-or-infinite magnitude
-// amax: 448 = 1.75 * 2^8, so amax = 1.M * 2^(E - 127) needs e = E - 135, one
-// more if 1.M > 1.75.  Zero vectors take scale 1.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// The exponent byte of a vector with largest magnitude amax (NaN if it holds
+// one): 448 = 1.75 * 2^8, so amax = 1.M * 2^(E - 127) needs e = E - 135, one more
+// if 1.M > 1.75.  Zero vectors take scale 1.
 __device__ __forceinline__ uint32_t exp_byte(float amax) {
   const uint32_t u = __float_as_uint(amax);
   if (u == 0) return 127u;
+  if (u > 0x7F800000u) return 255u;
   const int byte = (int)(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   return (uint32_t)max(byte, 1);
 }
@@ -186,18 +194,19 @@ __global__ void __launch_bounds__(kCacheThreads)
       if constexpr (kIsE4M3<TC>) {
         float ka = 0.f, va = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {        // fmaxf drops a NaN
-          ka = fmaxf(ka, fabsf(kx[i].x[e]));
-          va = fmaxf(va, fabsf(vx[i].x[e]));
+        for (int e = 0; e < 8; ++e) {
+          ka = max_nan(ka, fabsf(kx[i].x[e]));
+          va = max_nan(va, fabsf(vx[i].x[e]));
         }
         for (int off = lpv >> 1; off > 0; off >>= 1) {
-          ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, off));
-          va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, off));
+          ka = max_nan(ka, __shfl_xor_sync(0xffffffffu, ka, off));
+          va = max_nan(va, __shfl_xor_sync(0xffffffffu, va, off));
         }
         const uint32_t kb = exp_byte(ka), vb = exp_byte(va);
-        // 2^-e = 2^(127 - byte): biased exponent 254 - byte, in [7, 253]
-        const float ks = __uint_as_float((254u - kb) << 23);
-        const float vs = __uint_as_float((254u - vb) << 23);
+        // 2^-e = 2^(127 - byte): biased exponent 254 - byte, in [7, 253] (a NaN
+        // vector: 0, what it holds does not matter)
+        const float ks = __uint_as_float((254u - min(kb, 254u)) << 23);
+        const float vs = __uint_as_float((254u - min(vb, 254u)) << 23);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           kx[i].x[e] *= ks;

@@ -37,9 +37,10 @@ __device__ __forceinline__ uint16_t float2_to_e4m3x2(float lo, float hi) {
   return r;
 }
 
-// 2^(byte - 127): exact; byte 0 is 2^-127 (subnormal).
+// 2^(byte - 127): exact; byte 0 is 2^-127 (subnormal), byte 255 NaN.
 __device__ __forceinline__ float exp_scale(uint32_t byte) {
-  return byte == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
+  return byte == 0 ? __uint_as_float(0x00400000u)
+                   : byte == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte << 23);
 }
 
 // Writing to and reading from the pages (cache.cu).
@@ -127,10 +128,13 @@ __device__ __forceinline__ bool in_window(int len, int i, int j, int window, int
 
 // bf16 queries, d = 256, G = Hq / Hkv in {1, 2, 4, 8, 16} on tcgen05
 // (paged_tc.cu).  Sequences are scheduled in groups of kPagedTcGroup.
-constexpr int kPagedTcGroup = 192;
+constexpr int kPagedTcGroup = 64;
 struct PagedTcParams : PagedParams {
+  CUtensorMap map_k, map_v;  // bf16 pools, if use_tma
+  int use_tma;
   float* ws;                 // partials [n_clusters * 2][256 rows][256], then (m, l)
-  int G, tok_per_tile;       // heads per kv head; new tokens per 256-row tile
+  int G, g_shift;            // heads per kv head (a power of two), its logarithm
+  int tok_per_tile;          // new tokens per 256-row tile
   int n_tiles;               // query tiles per (sequence, kv head)
   int b0, nb;                // this launch's sequences
   int n_clusters;

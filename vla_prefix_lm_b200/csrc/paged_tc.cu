@@ -10,17 +10,18 @@
 // as in the dense kernel (tc_pair.cu).  What differs is how keys arrive and how
 // the work is shared out.
 //
-// Loading.  Four loader warps per CTA gather rows by page into the operands'
-// 128-byte-swizzled layout: every lane looks up one row's slot, warps copy whole
-// rows (16 bytes per lane).  A tensor-map load would need one copy per page and
-// 64-column block (32 per tile at 16-token pages), could not hide a row that no
-// query sees, and its map costs the host more than the smallest call takes.
-// Rows past the length, outside the window or of padding tokens are written as
-// zeros, so whatever a stale slot holds (NaN) meets P = 0 as 0.
-//   bf16: cp.async, up to three items (K: 32 KB, half V: 16 KB) in flight.
+// Loading, by two warps per CTA and operand into the 128-byte-swizzled layout:
+//   bf16, tiles whose 128 keys are all seen by some query: TMA, one box of
+//     min(page, 64) rows per page (all columns of the item at once from 64-token
+//     pages on, else one 64-column block each), asynchronous to everything else.
+//   Other tiles (the ragged last one, the window's edges, the chunk's own):
+//     cp.async row by row, and zeros for rows past the length, outside the
+//     window or of padding tokens, so that whatever a stale slot holds (NaN)
+//     meets P = 0 as 0.  (Gathering every tile this way held a CTA to 11 bytes
+//     a cycle, about 5700 cycles a tile.)
 //   e4m3: 16-byte loads held in registers one tile ahead (32 KB raw per CTA in
-//   flight), then e4m3 -> fp16 -> fp32 * 2^e -> bf16.  Every step is exact, as
-//   the scale is a power of two: no rounding beside the cache's own.
+//     flight), then rebuilt as bf16 exactly, as the scale is a power of two: no
+//     rounding beside the cache's own.
 //
 // Work.  Unit = (sequence, kv head, query tile).  Lengths differ by sequence
 // and live on the device, so each cluster derives the schedule itself from
@@ -31,11 +32,17 @@
 // that paged_combine_kernel merges by the log-sum-exp rule.  No atomics: the
 // result does not depend on timing.
 //
-// Warp roles per CTA (384 threads, three warpgroups):
-//   warps 0..3   softmax, O correction, epilogue (240 registers)
-//   warps 4..7   loaders
-//   warp 8       TMEM allocation; QK issue (even CTA)
-//   warp 9       PV issue (even CTA)
+// Warp roles per CTA (512 threads):
+//   warps 0..7   softmax, O correction, epilogue: warp w has the 32 rows of
+//                TMEM quarter w % 4 and half w / 4 of the columns.  Two warps per
+//                quarter keep the exponentials (1024 cycles of the special-
+//                function units per tile) under the MMAs' time; each row's two
+//                threads exchange their maxima through S's columns.
+//   warps 8, 9   load Q and K;  warps 10, 11 load V
+//   warp 12      TMEM allocation; QK issue (even CTA)
+//   warp 13      PV issue (even CTA)
+//   warp 14      scheduler: derives the segments this cluster runs and hands
+//                them to the other warps through a two-entry ring
 // TMEM per CTA (512 columns): O fp32 [0,256) | S0 [256,384) | S1 [384,512).
 // Shared memory per CTA: Q 64 KB | K ring 2 x 32 KB | V ring 2 or 4 x 16 KB |
 // P 32 KB (also the output staging area) | control | chunk token codes.
@@ -50,7 +57,7 @@ namespace piattn {
 
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kBM = 128;                    // query rows per CTA (256 per pair)
 constexpr int kRowsTile = 2 * kBM;
 constexpr int kBN = 128;                    // keys per key tile
@@ -72,6 +79,23 @@ constexpr uint32_t kIdescQK = idesc_bf16_f32(2 * kBM, kBN, false, false);
 constexpr uint32_t kIdescPV = idesc_bf16_f32(2 * kBM, kD, false, true);
 constexpr uint32_t kColO = 0, kColS = 256;
 constexpr int kGroup = kPagedTcGroup;
+constexpr int kSegs = 2;                     // segment ring
+constexpr int kSegUsers = 14;                // warps that read it
+
+
+// A run of key tiles of one unit on this cluster.
+struct Segment {
+  int b, g, tile;            // sequence (absolute), kv head, query tile
+  int tq0, tq1;              // its first / last new token
+  int len;                   // cached tokens
+  int lo0, lo1;              // window start of the first / last token (cached positions)
+  int sink_tiles, win_tile;  // cached tiles [0, sink_tiles) and [win_tile, ...)
+  int n_cached, c0;          // number of cached tiles; first chunk tile
+  int it0, n;                // this run: tiles [it0, it0 + n) of the unit's list
+  int slot;                  // partial slot, -1: the unit runs whole here
+  uint32_t csq0, csq1;       // block index of the first / last token
+  int any_e;                 // an expert among the tokens
+};
 
 template <int kNV_, int kMaxTok_>
 struct Layout {
@@ -83,6 +107,13 @@ struct Layout {
   static constexpr int kOffCtl = kOffP + kPBytes;
 };
 
+// The schedule's inputs: nominal tiles before each sequence's units, lengths.
+struct Plan {
+  int cum[kGroup + 1];
+  int len[kGroup];
+  int max_nom;
+};
+
 template <class L>
 struct __align__(8) Smem {
   uint64_t q_full, q_empty;
@@ -91,11 +122,12 @@ struct __align__(8) Smem {
   uint64_t s_full[2], s_free[2];
   uint64_t p_full, o_done, o_free;
   uint64_t drain_qk, drain_pv;
+  uint64_t pair[4];                 // a quarter's two warps meet
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint32_t tmem_base;
   int abort;
-  int scan[kThreads / 32];
-  long long cum[kGroup + 1];        // nominal tiles before each sequence's units
-  int max_nom;
+  Plan plan;
+  Segment seg[kSegs];
   uint16_t tile_cs_first[L::kTiles];
   uint16_t tile_cs_last[L::kTiles];
   uint8_t tile_fast[L::kTiles];
@@ -121,14 +153,17 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, int* abort,
-                                              const DevCtl& ctl) {
-  if (mbar_try_wait(bar, parity)) return true;
+// Code size matters in this kernel: a dozen warps in seven roles share the
+// instruction caches, and with everything inlined and unrolled each role's loop
+// waited for its own instructions (a third of all stalls, and 1.6 times the
+// time with e4m3 pages).  What is rare or long is out of line.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int* abort, int* status,
+                                       unsigned long long limit) {
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity)) {
     if (*(volatile int*)abort) return false;
-    if ((unsigned long long)(clock64() - t0) > ctl.wait_limit) {
-      record_status(ctl, kStatusTimeout);
+    if ((unsigned long long)(clock64() - t0) > limit) {
+      atomicCAS(status, 0, kStatusTimeout);
       *(volatile int*)abort = 1;
       return false;
     }
@@ -136,10 +171,12 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, in
   return true;
 }
 
+// Warp-uniform bounded wait: every lane polls, all get the same answer.
 template <class SmemT>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, SmemT& sm,
                                           const DevCtl& ctl) {
-  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, &sm.abort, ctl));
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, wait_slow(bar, parity, &sm.abort, ctl.status, ctl.wait_limit));
 }
 
 // ------------------------------------------------------------ the schedule
@@ -156,119 +193,94 @@ __device__ __forceinline__ int nominal_tiles(const PagedTcParams& p, int n) {
   return t + (p.Sq + kBN - 1) / kBN;
 }
 
-// Block-wide: cum[0 .. nb] (tiles before each sequence) and the largest nominal
-// count, from cache_lens.  Every thread of the block calls it.
-template <int kT>
-__device__ void build_schedule(const PagedTcParams& p, const DevCtl& ctl, long long* cum,
-                               int* max_nom) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) *max_nom = 0;
-  __syncthreads();
-  if (warp == 0) {
-    long long carry = 0;
-    int top = 0;
-    bool bad = false;
-    const long long units = (long long)p.Hkv * p.n_tiles;
-    for (int base = 0; base < p.nb; base += 32) {
-      const int b = base + lane;
-      int nom = 0;
-      if (b < p.nb)
-        nom = nominal_tiles(p, cached_len(p.lens, p.b0 + b, p.max_pages, p.page_shift, bad));
-      top = max(top, nom);
-      long long x = units * nom;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, off);
-        if (lane >= off) x += y;
-      }
-      if (b < p.nb) cum[b + 1] = carry + x;
-      carry += __shfl_sync(0xffffffffu, x, 31);
+// Warp-collective: the plan of this launch's sequences, from cache_lens.  (The
+// host keeps the total below 2^31 by the size of a group.)
+__device__ __forceinline__ void make_plan(const PagedTcParams& p, const DevCtl& ctl, Plan& plan,
+                                          int lane) {
+  const int units = p.Hkv * p.n_tiles;
+  int carry = 0, top = 0;
+  bool bad = false;
+  for (int base = 0; base < p.nb; base += 32) {
+    const int b = base + lane;
+    int nom = 0, n = 0;
+    if (b < p.nb) {
+      n = cached_len(p.lens, p.b0 + b, p.max_pages, p.page_shift, bad);
+      nom = nominal_tiles(p, n);
     }
-    if (lane == 0) cum[0] = 0;
+    top = max(top, nom);
+    int x = units * nom;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-    if (lane == 0) *max_nom = top;
-    if (bad && blockIdx.x == 0) record_status(ctl, kStatusArg);
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
+    }
+    if (b < p.nb) {
+      plan.cum[b + 1] = carry + x;
+      plan.len[b] = n;
+    }
+    carry += __shfl_sync(0xffffffffu, x, 31);
   }
-  __syncthreads();
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+  if (lane == 0) {
+    plan.cum[0] = 0;
+    plan.max_nom = top;
+  }
+  if (bad && blockIdx.x == 0) record_status(ctl, kStatusArg);
+  __syncwarp();
 }
 
 // Tiles per cluster when the tiles are cut into equal ranges; 0: units run
 // whole, unit u on cluster u % n_clusters.  A cut costs a cluster about five
 // tiles' time (partials written and merged: measured against whole units at 32
 // sequences of 816 + 51 tokens), so units stay whole unless cutting saves that.
-__device__ __forceinline__ long long tiles_per_cluster(const PagedTcParams& p, long long total,
-                                                       int max_nom) {
+__device__ __forceinline__ int tiles_per_cluster(const PagedTcParams& p, const Plan& plan) {
   if (!p.may_cut) return 0;
-  const long long n_units = (long long)p.nb * p.Hkv * p.n_tiles;
-  const long long per = max((total + p.n_clusters - 1) / p.n_clusters, 2ll);
-  const long long rounds = (n_units + p.n_clusters - 1) / p.n_clusters;
-  return rounds * max_nom <= per + 5 ? 0 : per;
+  const int n_units = p.nb * p.Hkv * p.n_tiles;
+  const int per = max((plan.cum[p.nb] + p.n_clusters - 1) / p.n_clusters, 2);
+  const int rounds = (n_units + p.n_clusters - 1) / p.n_clusters;
+  return (long long)rounds * plan.max_nom <= per + 5 ? 0 : per;
 }
 
-// A run of key tiles of one unit on this cluster.
-struct Segment {
-  int b, g, tile;            // sequence (absolute), kv head, query tile
-  int tq0, tq1;              // its first / last new token
-  int len;                   // cached tokens
-  int lo0, lo1;              // window start of the first / last token (cached positions)
-  int sink_tiles, win_tile;  // cached tiles [0, sink_tiles) and [win_tile, ...)
-  int n_cached, c0;          // number of cached tiles; first chunk tile
-  int it0, n;                // this run: tiles [it0, it0 + n) of the unit's list
-  int slot;                  // partial slot, -1: the unit runs whole here
-  uint32_t csq0, csq1;       // block index of the first / last token
-  bool any_e;                // an expert among the tokens
+// The next segment's place in the schedule: unit (b, g, tile) and the nominal
+// range [s0, s1) of its nom tiles.  pos: a tile of the cluster's range, or with
+// per == 0 a unit.  Returns the position after it.
+struct Place {
+  int b, g, tile, slot, s0, s1, nom;
 };
-
-// Where the walk over this cluster's segments stands.
-struct Walk {
-  long long pos, end, step;  // cut: tile range; whole: unit index, count, stride
-  int seg;
-};
-
-template <class SmemT>
-__device__ __forceinline__ int find_seq(const SmemT& sm, int nb, long long pos) {
-  int lo = 0, hi = nb - 1;                   // largest b with cum[b] <= pos
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (sm.cum[mid] <= pos) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
-}
-
-// Takes the next segment's place in the schedule: b, g, tile and the nominal
-// range [s0, s1) of nom tiles.  False when the cluster is done.
-template <class SmemT>
-__device__ bool next_place(const PagedTcParams& p, const SmemT& sm, long long per, Walk& w,
-                           Segment& x, int& s0, int& s1, int& nom) {
-  if (w.pos >= w.end) return false;
+__device__ __forceinline__ int next_place(const PagedTcParams& p, const Plan& plan, int per,
+                                          int pos, int end, Place& x) {
   const int units = p.Hkv * p.n_tiles;
-  long long u;
-  int b;
+  int b, u;
   if (per == 0) {
-    b = (int)(w.pos / units);
-    u = w.pos % units;
-    nom = (int)((sm.cum[b + 1] - sm.cum[b]) / units);
-    s0 = 0;
-    s1 = nom;
+    b = pos / units;
+    u = pos - b * units;
+    x.nom = (plan.cum[b + 1] - plan.cum[b]) / units;
+    x.s0 = 0;
+    x.s1 = x.nom;
     x.slot = -1;
-    w.pos += w.step;
+    pos += p.n_clusters;
   } else {
-    b = find_seq(sm, p.nb, w.pos);
-    nom = (int)((sm.cum[b + 1] - sm.cum[b]) / units);
-    const long long rem = w.pos - sm.cum[b];
-    u = rem / nom;
-    s0 = (int)(rem % nom);
-    s1 = (int)min((long long)nom, s0 + (w.end - w.pos));
+    int lo = 0, hi = p.nb - 1;               // largest b with cum[b] <= pos
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (plan.cum[mid] <= pos) lo = mid;
+      else hi = mid - 1;
+    }
+    b = lo;
+    x.nom = (plan.cum[b + 1] - plan.cum[b]) / units;
+    const int rem = pos - plan.cum[b];
+    u = rem / x.nom;
+    x.s0 = rem - u * x.nom;
+    x.s1 = min(x.nom, x.s0 + (end - pos));
     // A run that begins mid-unit is its cluster's first: slot 0, else slot 1.
-    x.slot = s0 == 0 && s1 == nom ? -1 : (int)(w.pos / per) * 2 + (s0 > 0 ? 0 : 1);
-    w.pos += s1 - s0;
+    x.slot = x.s0 == 0 && x.s1 == x.nom ? -1 : (pos / per) * 2 + (x.s0 > 0 ? 0 : 1);
+    pos += x.s1 - x.s0;
   }
-  x.b = p.b0 + b;
-  x.g = (int)(u / p.n_tiles);
-  x.tile = (int)(u % p.n_tiles);
-  return true;
+  x.b = b;
+  x.g = u / p.n_tiles;
+  x.tile = u - x.g * p.n_tiles;
+  return pos;
 }
 
 __device__ __forceinline__ int window_lo(const PagedTcParams& p, int len, int i) {
@@ -282,12 +294,16 @@ __device__ __forceinline__ int window_lo(const PagedTcParams& p, int len, int i)
 // element.)  A unit of padding rows has no tile.
 template <class SmemT>
 __device__ __forceinline__ void fill_segment(const PagedTcParams& p, const SmemT& sm,
-                                          const uint16_t* codes, Segment& x, int s0, int s1,
-                                          int nom, int lane) {
+                                          const uint16_t* codes, const Place& pl, Segment& out,
+                                          int lane) {
+  Segment x;
+  x.b = p.b0 + pl.b;
+  x.g = pl.g;
+  x.tile = pl.tile;
+  x.slot = pl.slot;
   x.tq0 = x.tile * p.tok_per_tile;
   x.tq1 = min(x.tq0 + p.tok_per_tile, p.Sq) - 1;
-  bool bad = false;
-  x.len = cached_len(p.lens, x.b, p.max_pages, p.page_shift, bad);
+  x.len = sm.plan.len[pl.b];
   int any_e = 0, any_live = 0;
   for (int t = x.tq0 + lane; t <= x.tq1; t += 32) {
     const uint32_t c = codes[t];
@@ -314,8 +330,9 @@ __device__ __forceinline__ void fill_segment(const PagedTcParams& p, const SmemT
     c1 += __popc(m);
   }
   const int total = live ? x.n_cached + max(c1 - x.c0, 0) : 0;
-  x.it0 = (int)((long long)s0 * total / nom);
-  x.n = (int)((long long)s1 * total / nom) - x.it0;
+  x.it0 = (int)((long long)pl.s0 * total / pl.nom);
+  x.n = (int)((long long)pl.s1 * total / pl.nom) - x.it0;
+  if (lane == 0) out = x;
 }
 
 struct KeyTile {
@@ -325,6 +342,96 @@ struct KeyTile {
 __device__ __forceinline__ KeyTile key_tile(const Segment& x, int idx) {
   if (idx >= x.n_cached) return {x.c0 + idx - x.n_cached, true};
   return {idx < x.sink_tiles ? idx : x.win_tile + idx - x.sink_tiles, false};
+}
+// Whether every key of a cached tile is seen by some query of the segment.
+__device__ __forceinline__ bool whole_tile(const PagedTcParams& p, const Segment& x,
+                                           const KeyTile& kt) {
+  const int k0 = kt.tile * kBN;
+  return !kt.chunk && k0 + kBN <= x.len && (p.window <= 0 || k0 >= x.lo0 || k0 + kBN <= p.sinks);
+}
+
+// Warp-collective: the codes of sequence b's chunk and each tile's summary, a
+// tile of 128 tokens at a time.  (A short loop: its code is fetched cold by
+// every call, and the whole kernel waits for it.)
+template <class SmemT>
+__device__ __forceinline__ void scan_codes(const PagedTcParams& p, SmemT& sm, uint16_t* codes,
+                                           int b, int lane) {
+  const uint8_t* ar = p.ar + (long long)b * p.mask_bs;
+  const int32_t* seg = p.seg ? p.seg + (long long)b * p.mask_bs : nullptr;
+  uint32_t cs = 0;
+#pragma unroll 1
+  for (int t0 = 0; t0 < p.Sq; t0 += kBN) {
+    uint32_t on[4];
+    int sg[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = t0 + 32 * i + lane;
+      on[i] = t < p.Sq ? ar[t] : 0u;
+      sg[i] = t < p.Sq && seg ? seg[t] : 0;
+    }
+    uint32_t any_f = 0, all_f = ~0u, any_p = 0, all_p = ~0u;
+    uint32_t first = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = t0 + 32 * i + lane;
+      const uint32_t m = __ballot_sync(0xffffffffu, on[i] != 0u);
+      const uint32_t code =
+          t < p.Sq ? make_code(cs + __popc(m & (0xffffffffu >> (31 - lane))), sg[i]) : 0xFFFFu;
+      codes[t] = (uint16_t)code;
+      if (i == 0) first = cs + (m & 1u);
+      cs += __popc(m);
+      const uint32_t live = __ballot_sync(0xffffffffu, t < p.Sq);
+      const uint32_t f = __ballot_sync(0xffffffffu, (code & 1u) != 0u) & live;
+      const uint32_t q = __ballot_sync(0xffffffffu, is_pad(code)) & live;
+      any_f |= f;
+      all_f &= f | ~live;
+      any_p |= q;
+      all_p &= q | ~live;
+    }
+    if (lane == 0) {
+      sm.tile_cs_first[t0 / kBN] = (uint16_t)first;
+      sm.tile_cs_last[t0 / kBN] = (uint16_t)cs;
+      sm.tile_fast[t0 / kBN] = (uint8_t)((any_f ? 1u : 0u) | (all_f == ~0u ? 2u : 0u) |
+                                         (any_p ? 4u : 0u) | (all_p == ~0u ? 8u : 0u));
+    }
+  }
+  __syncwarp();
+}
+
+// Which of the 64 keys from tile offset 64 * half a query row sees, one bit
+// each.  tok: the row's token (its code cq).
+__device__ __noinline__ uint2 row_mask(const PagedTcParams& p, const uint16_t* codes,
+                                       const Segment& x, bool chunk, int h0, int tok, uint32_t cq) {
+  const int lane = threadIdx.x & 31;
+  uint32_t vm[2] = {~0u, ~0u};
+  int a, e, s;                               // visible: [a, e) and [0, s) from h0
+  if (chunk) {
+    e = 0;                                   // keys whose block the row admits: a prefix
+#pragma unroll 1
+    for (int step = 64; step >= 1; step >>= 1) {
+      const int probe = e + step;
+      if (probe <= 64 && (uint32_t)(codes[h0 + probe - 1] >> 2) <= (cq >> 2)) e = probe;
+    }
+    e = min(e, p.Sq - h0);
+    a = p.window > 0 ? tok - p.window + 1 - h0 : 0;
+    s = p.window > 0 ? min(max(p.sinks - x.len, 0) - h0, e) : 0;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      // FAST bit (padding keys carry it too) and padding, per key
+      const uint32_t ck = codes[h0 + 32 * w + lane];
+      const uint32_t fw = __ballot_sync(0xffffffffu, (ck & 1u) != 0u);
+      const uint32_t pw = __ballot_sync(0xffffffffu, is_pad(ck));
+      vm[w] = ~((cq & 2u) ? fw : pw);
+    }
+  } else {
+    e = x.len - h0;
+    a = window_lo(p, x.len, tok) - h0;       // below: sinks only
+    s = p.window > 0 ? min(p.sinks, x.len) - h0 : 0;
+  }
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+    vm[w] &= (bits_below(e - 32 * w) & ~bits_below(a - 32 * w)) | bits_below(s - 32 * w);
+  return make_uint2(vm[0], vm[1]);
 }
 
 // ------------------------------------------------------------- the loaders
@@ -341,17 +448,19 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The cache slot of cached position x, -1 if no query of the segment sees it
-// (or its page id is out of range, which is recorded).
-__device__ __forceinline__ int cached_slot(const PagedTcParams& p, const Segment& s, int x,
-                                           bool& bad) {
-  if (x >= s.len || (p.window > 0 && x < s.lo0 && x >= p.sinks)) return -1;
-  const int page = p.table[(long long)s.b * p.max_pages + (x >> p.page_shift)];
-  if (page < 0 || page >= p.num_pages) {
-    bad = true;
-    return -1;
-  }
-  return (page << p.page_shift) + (x & ((1 << p.page_shift) - 1));
+// Cached position x: the page id that holds it, kNoRow if no query of the
+// segment sees it.  Loaded a tile before row_of() uses it.
+constexpr int kNoRow = -2147483647 - 1;
+__device__ __forceinline__ int page_of(const PagedTcParams& p, const Segment& s, int x) {
+  if (x >= s.len || (p.window > 0 && x < s.lo0 && x >= p.sinks)) return kNoRow;
+  return p.table[(long long)s.b * p.max_pages + (x >> p.page_shift)];
+}
+// Its slot; -1 if there is none (a page id out of range is noted in bad).
+__device__ __forceinline__ int slot_of(const PagedTcParams& p, int x, int page, bool& bad) {
+  if (page >= 0 && page < p.num_pages)
+    return (page << p.page_shift) + (x & ((1 << p.page_shift) - 1));
+  bad = bad || page != kNoRow;
+  return -1;
 }
 
 // The row of chunk key j in [B * Sq], -1 if it is padding, out of the chunk or
@@ -364,14 +473,129 @@ __device__ __forceinline__ int chunk_row(const PagedTcParams& p, const Segment& 
   return s.b * p.Sq + j;
 }
 
-// Eight raw e4m3 -> four bf16x2 words, times 2^(byte - 127): exact.
-__device__ __forceinline__ void dequant8(uint32_t w0, uint32_t w1, float2 sc, uint32_t (&o)[4]) {
-  const uint32_t w[2] = {w0, w1};
+// Four raw e4m3 -> two bf16x2 words, times 2^(byte - 127), exact.  The byte's
+// exponent and mantissa moved to bf16's places read as the value times 2^-120
+// (subnormals too); the multiplication by m = 2^(byte - 7) undoes that and applies
+// the scale.  Integer and fp16-pipe instructions only: the conversion
+// instructions run at a quarter of their rate, on the units that the softmax's
+// exponentials need (7600 cycles a tile with them, 3 times the MMAs' time).
+__device__ __forceinline__ uint2 dequant4(uint32_t w, uint32_t m) {
+  uint2 o;
+  const uint32_t x0 = __byte_perm(w, 0u, 0x1404), x1 = __byte_perm(w, 0u, 0x3424);
+  const uint32_t y0 = ((x0 >> 4) & 0x07f007f0u) | (x0 & 0x80008000u);
+  const uint32_t y1 = ((x1 >> 4) & 0x07f007f0u) | (x1 & 0x80008000u);
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.x) : "r"(y0), "r"(m));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.y) : "r"(y1), "r"(m));
+  return o;
+}
+// bf16x2 of 2^(byte - 7) twice (at most 2^127: rest_scale has what is missing);
+// NaN for byte 255, 0 where there is no row.
+constexpr uint32_t kNoExp = 256u;
+__device__ __forceinline__ uint32_t main_scale(uint32_t byte) {
+  const uint32_t f = byte == kNoExp ? 0u : byte == 255u ? 0x7FC0u : min(byte + 120u, 254u) << 7;
+  return f * 0x10001u;
+}
+// Scales above 2^7 (values above 448 * 2^7): bf16x2 of 2^(byte - 134).
+__device__ __forceinline__ uint32_t rest_scale(uint32_t byte) {
+  return ((byte >= 255u || byte <= 134u ? 127u : byte - 7u) << 7) * 0x10001u;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t o;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(a), "r"(b));
+  return o;
+}
+
+// n rows of an item by cp.async, zeros where there is none: row row0 + i * step
+// is row __shfl(mine, lane0 + i * lane_step) of the tensor at base.
+__device__ __noinline__ void copy_rows(int mine, const uint8_t* base, uint32_t pitch, uint32_t dst,
+                                       int n, int row0, int step, int lane0, int lane_step) {
+  const int c = threadIdx.x & 7;
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += 8) {
+    int r[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 v = fmul2(e4m3x2_to_float2((uint16_t)(w[i >> 1] >> (16 * (i & 1)))), sc);
-    o[i] = cvt_bf16x2(v.x, v.y);
+    for (int i = 0; i < 8; ++i) r[i] = __shfl_sync(0xffffffffu, mine, lane0 + (i0 + i) * lane_step);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = row0 + (i0 + i) * step;
+      cp_async16(dst + row * 128 + ((c ^ (row & 7)) << 4),
+                 base + (unsigned long long)(uint32_t)max(r[i], 0) * pitch, r[i] >= 0);
+    }
   }
+}
+
+// 16 raw bytes of each of two rows -> two 16-byte chunks of bf16 each, at shared
+// addresses a0, a1 and b0, b1; m: their scales (main_scale).  Not inlined: the
+// loaders' unrolled conversions (16 KB of code a warp) beside the softmax's
+// starved every warp of instructions.
+template <bool kRest>
+__device__ __noinline__ void put_pair(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1, uint4 wa,
+                                      uint4 wb, uint32_t ma, uint32_t mb, uint32_t ra, uint32_t rb) {
+  uint2 qa[4] = {dequant4(wa.x, ma), dequant4(wa.y, ma), dequant4(wa.z, ma), dequant4(wa.w, ma)};
+  uint2 qb[4] = {dequant4(wb.x, mb), dequant4(wb.y, mb), dequant4(wb.z, mb), dequant4(wb.w, mb)};
+  if (kRest) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      qa[i] = make_uint2(mul_bf16x2(qa[i].x, ra), mul_bf16x2(qa[i].y, ra));
+      qb[i] = make_uint2(mul_bf16x2(qb[i].x, rb), mul_bf16x2(qb[i].y, rb));
+    }
+  }
+  st_shared_v4(a0, make_uint4(qa[0].x, qa[0].y, qa[1].x, qa[1].y));
+  st_shared_v4(a1, make_uint4(qa[2].x, qa[2].y, qa[3].x, qa[3].y));
+  st_shared_v4(b0, make_uint4(qb[0].x, qb[0].y, qb[1].x, qb[1].y));
+  st_shared_v4(b1, make_uint4(qb[2].x, qb[2].y, qb[3].x, qb[3].y));
+}
+// The N pieces that fetch_rows brought -> an item.  Lane: 16 bytes c16 of row
+// row0 + it * step; scale and exponent of row it sit in lane lane0 + it * lstep.
+template <int N>
+__device__ __forceinline__ void put_rows(uint32_t item, int row0, int step, int c16, int lane0,
+                                         int lstep, const uint4 (&raw)[N], uint32_t e) {
+  const uint32_t m = main_scale(e);
+  const uint32_t base = item + row0 * 128 + (c16 >> 2) * kKBlk;
+  const int c = (c16 & 3) * 2, x0 = row0 & 7, x1 = (row0 + step) & 7;
+  const uint32_t a0 = base + ((c ^ x0) << 4), a1 = base + (((c + 1) ^ x0) << 4);
+  const uint32_t b0 = base + step * 128 + ((c ^ x1) << 4),
+                 b1 = base + step * 128 + (((c + 1) ^ x1) << 4);
+  const bool rest = __any_sync(0xffffffffu, e > 134u && e != kNoExp);     // values above 448 * 2^7
+  const uint32_t r = rest ? rest_scale(e) : 0u;
+#pragma unroll
+  for (int it = 0; it < N; it += 2) {
+    const uint32_t d = it * step * 128;      // (2 * step is a multiple of 8 rows)
+    const uint32_t ma = __shfl_sync(0xffffffffu, m, lane0 + it * lstep);
+    const uint32_t mb = __shfl_sync(0xffffffffu, m, lane0 + (it + 1) * lstep);
+    if (!rest) {
+      put_pair<false>(a0 + d, a1 + d, b0 + d, b1 + d, raw[it], raw[it + 1], ma, mb, 0u, 0u);
+    } else {
+      const uint32_t ra = __shfl_sync(0xffffffffu, r, lane0 + it * lstep);
+      const uint32_t rb = __shfl_sync(0xffffffffu, r, lane0 + (it + 1) * lstep);
+      put_pair<true>(a0 + d, a1 + d, b0 + d, b1 + d, raw[it], raw[it + 1], ma, mb, ra, rb);
+    }
+  }
+}
+
+// N raw pieces of 16 bytes at byte `col` of the rows row_at(0 .. N - 1) of an
+// e4m3 pool.  Rows below 0 read row 0: their scale is 0, and every byte
+// dequantises to a finite number.
+template <int N, class RowAt>
+__device__ __forceinline__ void fetch_rows(const PagedTcParams& p, const void* pool, int col,
+                                           int g, uint4 (&raw)[N], RowAt row_at) {
+  if (p.num_pages == 0) {                    // no row 0 either
+#pragma unroll
+    for (int it = 0; it < N; ++it) raw[it] = make_uint4(0u, 0u, 0u, 0u);
+    return;
+  }
+  const uint8_t* base = static_cast<const uint8_t*>(pool) + g * kD + col;
+  const uint32_t pitch = (uint32_t)p.Hkv * kD;
+  int r[N];
+#pragma unroll
+  for (int it = 0; it < N; ++it) r[it] = max(row_at(it), 0);
+#pragma unroll
+  for (int it = 0; it < N; ++it)
+    raw[it] = __ldg(reinterpret_cast<const uint4*>(base + (unsigned long long)(uint32_t)r[it] * pitch));
+}
+// The exponent byte of row r, loaded by the lane that looked the row up.
+__device__ __forceinline__ uint32_t row_exp(const PagedTcParams& p, const uint8_t* exps, int r, int g) {
+  return r >= 0 ? (uint32_t)__ldg(exps + (unsigned long long)(uint32_t)r * (uint32_t)p.Hkv + g) : kNoExp;
 }
 
 template <bool kE4M3, class L>
@@ -401,87 +625,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int cluster = blockIdx.x >> 1;
 
   if (threadIdx.x == 0) {
-    mbar_init(&sm.q_full, 8);
+    mbar_init(&sm.q_full, 4);
     mbar_init(&sm.q_empty, 1);
     for (int s = 0; s < kNK; ++s) {
-      mbar_init(&sm.k_full[s], 8);
+      mbar_init(&sm.k_full[s], 4);
       mbar_init(&sm.k_empty[s], 1);
     }
     for (int s = 0; s < kNV; ++s) {
-      mbar_init(&sm.v_full[s], 8);
+      mbar_init(&sm.v_full[s], 4);
       mbar_init(&sm.v_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.s_full[s], 1);
-      mbar_init(&sm.s_free[s], 8);
+      mbar_init(&sm.s_free[s], 16);
     }
-    mbar_init(&sm.p_full, 8);
+    mbar_init(&sm.p_full, 16);
     mbar_init(&sm.o_done, 1);
-    mbar_init(&sm.o_free, 8);
+    mbar_init(&sm.o_free, 16);
     mbar_init(&sm.drain_qk, 1);
     mbar_init(&sm.drain_pv, 1);
+    for (int s = 0; s < 4; ++s) mbar_init(&sm.pair[s], 2);
+    for (int s = 0; s < kSegs; ++s) {
+      mbar_init(&sm.seg_full[s], 1);
+      mbar_init(&sm.seg_empty[s], kSegUsers);
+    }
     sm.abort = 0;
     fence_barrier_init();
   }
   cluster_sync();                             // both CTAs' barriers exist
-  if (warp == 8) {
+  if (warp == 12) {
     tmem_alloc_pair(&sm.tmem_base, 512);
     tmem_relinquish_pair();
   }
-  pdl_wait();
-  pdl_launch_dependents();
-  build_schedule<kThreads>(p, ctl, sm.cum, &sm.max_nom);
-  const long long per = tiles_per_cluster(p, sm.cum[p.nb], sm.max_nom);
-  Walk walk;
-  if (per == 0) {
-    walk = {cluster, (long long)p.nb * p.Hkv * p.n_tiles, p.n_clusters, 0};
-  } else {
-    walk = {min(cluster * per, sm.cum[p.nb]), min((cluster + 1) * per, sm.cum[p.nb]), 0, 0};
-  }
-
-  // Block-wide: the codes of sequence b's chunk.
-  int codes_b = -1;
-  auto scan_codes = [&](int b) {
-    const uint8_t* ar = p.ar + (long long)b * p.mask_bs;
-    const int32_t* seg = p.seg ? p.seg + (long long)b * p.mask_bs : nullptr;
-    const Flags32 f0 = load_flags32(ar, seg, p.Sq, (int)threadIdx.x * 32);
-    __syncthreads();                          // nobody reads the old codes any more
-    build_codes_x32<kThreads>(ar, seg, p.Sq, pad_tokens(p.Sq), codes, sm.scan, f0,
-                              TileSums{sm.tile_cs_first, sm.tile_cs_last, sm.tile_fast});
-    codes_b = b;
-  };
-  if (p.mask_bs == 0) scan_codes(0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // Every warp walks the same segments; with a mask per sequence all of them
-  // meet to scan the next sequence's (after a failure too, so that no one waits
-  // for a warp that gave up).
-  auto next_segment = [&](Segment& x) -> bool {
-    int s0, s1, nom;
-    if (!next_place(p, sm, per, walk, x, s0, s1, nom)) return false;
-    if (p.mask_bs != 0 && x.b != codes_b) scan_codes(x.b);
-    fill_segment(p, sm, codes, x, s0, s1, nom, lane);
-    return true;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // Every other warp takes the scheduler's segments in order; null at the end
+  // (or after a failure).
+  bool ok = true;
+  uint32_t n_seg = 0;
+  auto next_segment = [&]() -> const Segment* {
+    if (n_seg > 0) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.seg_empty[(n_seg - 1) % kSegs]);
+    }
+    const int i = (int)(n_seg % kSegs);
+    if (!ok || !warp_wait(&sm.seg_full[i], (n_seg / kSegs) & 1, sm, ctl)) return nullptr;
+    ++n_seg;
+    return sm.seg[i].n < 0 ? nullptr : &sm.seg[i];
   };
 
   const uint32_t tmem = sm.tmem_base;
   const uint32_t tO = tmem + kColO, tS = tmem + kColS;      // S[b] at +128 b
-  bool ok = true;
-  Segment x;
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  if (warp >= 12) {
     auto commit_both = [&](uint64_t* bar) {
       umma_commit_pair(mapa_shared(smem_u32(bar), 0));
       umma_commit_pair(mapa_shared(smem_u32(bar), 1));
     };
     uint32_t gt = 0, nu = 0;      // key tiles and segments processed
-    if (warp == 8) {
+    if (warp == 12) {
       const uint64_t qdesc0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t kdesc0 = sdesc_sw128(smem_u32(kring), 16, 1024);
-      while (next_segment(x)) {
-        if (!leader || !ok || x.n == 0) continue;
+      while (const Segment* px = next_segment()) {
+        const Segment& x = *px;
+        if (!leader || x.n == 0) continue;
         ok = warp_wait(&sm.q_full, nu & 1, sm, ctl);
         ++nu;
         for (int j = 0; j < x.n && ok; ++j, ++gt) {
@@ -493,7 +704,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc_fence_after();
           if (lane == 0) {
             const uint64_t kd = kdesc0 + (uint64_t)((s * kKItem) >> 4);
-#pragma unroll
+#pragma unroll 4
             for (int kk = 0; kk < kD / 16; ++kk) {
               const uint32_t qoff = (uint32_t)((kk >> 2) * kQBlk + (kk & 3) * 32);
               const uint32_t koff = (uint32_t)((kk >> 2) * kKBlk + (kk & 3) * 32);
@@ -512,12 +723,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         (void)mbar_wait(&sm.drain_qk, 0, ctl);
       }
-    } else if (warp == 9) {
+    } else if (warp == 13) {
       const uint64_t pdesc0 = sdesc_sw128(smem_u32(sP), 16, 1024);
       const uint64_t vdesc0 = sdesc_sw128(smem_u32(vring), kKBlk, 1024);
       uint32_t uv = 0;
-      while (next_segment(x)) {
-        if (!leader || !ok || x.n == 0) continue;
+      while (const Segment* px = next_segment()) {
+        const Segment& x = *px;
+        if (!leader || x.n == 0) continue;
         ++nu;
         for (int j = 0; j < x.n && ok; ++j, ++gt) {
           // V arrives before P: wait for it first, off the critical path.
@@ -551,16 +763,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         (void)mbar_wait(&sm.drain_pv, 0, ctl);
       }
-    } else {
-      while (next_segment(x)) {
+    } else if (warp == 14) {
+      // ------------------------------------------------------ scheduler
+      if (p.mask_bs == 0) scan_codes(p, sm, codes, 0, lane);
+      make_plan(p, ctl, sm.plan, lane);
+      const int per = tiles_per_cluster(p, sm.plan);
+      const int step = per == 0 ? p.nb * p.Hkv * p.n_tiles : sm.plan.cum[p.nb];
+      int pos = per == 0 ? cluster : min((int)min((long long)cluster * per, (long long)step), step);
+      const int end = per == 0 ? step : (int)min((long long)pos + per, (long long)step);
+      int codes_b = -1;
+      // A ring entry is free once the users of the segment kSegs back are done.
+      auto released = [&](uint32_t k) {      // segment k's entry, by its users
+        return warp_wait(&sm.seg_empty[k % kSegs], (k / kSegs) & 1, sm, ctl);
+      };
+      for (;;) {
+        if (n_seg >= kSegs && !released(n_seg - kSegs)) break;
+        Segment& out = sm.seg[n_seg % kSegs];
+        const bool done = pos >= end;
+        if (done) {
+          if (lane == 0) out.n = -1;
+        } else {
+          Place pl;
+          pos = next_place(p, sm.plan, per, pos, end, pl);
+          if (p.mask_bs != 0 && pl.b != codes_b) {
+            // Nobody may still read the old codes.
+            if (n_seg > 0 && !released(n_seg - 1)) break;
+            scan_codes(p, sm, codes, p.b0 + pl.b, lane);
+            codes_b = pl.b;
+          }
+          fill_segment(p, sm, codes, pl, out, lane);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.seg_full[n_seg % kSegs]);
+        ++n_seg;
+        if (done) break;
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 8) {
     // ---------------------------------------------------------- loaders
-    const int lw = warp - 4;
+    // Warps 8 and 9 bring Q and K, warps 10 and 11 V: a warp that waits for its
+    // copies to land must not hold back the other operand's.
+    const int lw = warp & 1;
+    const Segment* px = nullptr;
     bool bad = false;
-    uint32_t uk = 0, uv = 0, nq = 0;
-    const uint32_t kring_u = smem_u32(kring), vring_u = smem_u32(vring), sQ_u = smem_u32(sQ);
     // Full barriers (even CTA) of the cp.async items in flight, oldest first.
     uint32_t pend0 = 0, pend1 = 0;
     int n_pend = 0;
@@ -591,236 +836,284 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto acquire = [&](uint64_t* bar, uint32_t use) -> bool {   // use: earlier fills of the slot
       if (use == 0) return true;
       const uint32_t parity = (use - 1) & 1;
-      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-      flush();
+      if (n_pend > 0) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        flush();
+      }
       return warp_wait(bar, parity, sm, ctl);
+    };
+    // Waits (bounded) for the last phase of a ring's full barriers, so that no
+    // copy into either CTA is in flight when the cluster leaves; phases that the
+    // consumer has waited for return at once.
+    auto land = [&](uint64_t* full, int slots, uint32_t used) {
+      flush();
+      if (leader && lw == 0 && lane == 0)
+        for (int s = 0; s < slots; ++s) {
+          const uint32_t n = used > (uint32_t)s ? (used - (uint32_t)s + slots - 1) / slots : 0;
+          if (n > 0) (void)mbar_wait(&full[s], (n - 1) & 1, ctl);
+        }
+      __syncwarp();
     };
     auto bar_full = [&](uint64_t* bar) { return mapa_shared(smem_u32(bar), 0); };
 
-    // Row lookup: lane l < 16 holds the l-th of the 16 rows this warp copies.
-    // K: this CTA's rows l * 4 + lw of the tile; V half h: (l / 2) * 8 + lw * 2
-    // + l % 2.  Cached rows are slots, chunk rows are rows of k_new.
-    auto lookup = [&](const KeyTile& kt, int row) -> int {
-      const int at = kt.tile * kBN + row;
-      return kt.chunk ? chunk_row(p, x, codes, at) : cached_slot(p, x, at, bad);
+    // Row lookup: lane l looks up the l-th of the 32 rows (of 64) that this warp
+    // copies of an item; rows of 512 bytes take all 32 lanes, of 256 bytes 16
+    // lanes, of 128 bytes 8 lanes.  Page ids are loaded a tile ahead (peek), so
+    // that their latency does not delay the copies.
+    const int row32 = lane * 2 + lw;                               // 32 lanes per row
+    const int row16 = (lane >> 1) * 4 + lw * 2 + (lane & 1);       // 16
+    const int row8 = (lane >> 2) * 8 + lw * 4 + (lane & 3);        // 8
+    // e4m3: which of a pass's rows, and which 16-byte piece, this lane has.  Each
+    // eight lanes hold four pieces of two adjacent rows, whose bf16 chunks fall
+    // on eight different bank groups.
+    const int odd = (lane >> 2) & 1;
+    const int sub16 = odd, piece16 = (lane & 3) + 4 * (lane >> 3);
+    const int sub8 = odd + 2 * (lane >> 4), piece8 = (lane & 3) + 4 * ((lane >> 3) & 1);
+    // TMA tiles: lane l has the page of box l.
+    const int box = min(1 << p.page_shift, 64);                    // rows per box
+    const int boxes = 64 / box;                                    // per 64 keys
+    auto peek = [&](int idx, int row, int tma_row) -> int {
+      if (idx >= px->it0 + px->n) return kNoRow;
+      const KeyTile kt = key_tile(*px, idx);
+      if (kt.chunk) return kNoRow;
+      const bool tma = !kE4M3 && p.use_tma && whole_tile(p, *px, kt);
+      return page_of(p, *px, kt.tile * kBN + (tma ? tma_row : row));
     };
-    auto copy_k = [&](const KeyTile& kt, int s) {
-      const int mine = lane < 16 ? lookup(kt, 64 * (int)rank + lane * 4 + lw) : -1;
-      const uint8_t* base = static_cast<const uint8_t*>(kt.chunk ? p.k : p.kp) + lane * 16;
-      const uint32_t dst0 = kring_u + s * kKItem + (lane >> 3) * kKBlk;
-#pragma unroll
-      for (int it = 0; it < 16; ++it) {
-        const int r = __shfl_sync(0xffffffffu, mine, it);
-        const int row = it * 4 + lw;
-        cp_async16(dst0 + row * 128 + (((lane & 7) ^ (row & 7)) << 4),
-                   base + ((long long)max(r, 0) * p.Hkv + x.g) * (kD * 2), r >= 0);
+    // The boxes of one item: `blocks` 64-column blocks from block c0 of the
+    // head, keys from position x0; lane l brings box l / blocks, block l % blocks
+    // (pages of 64 tokens and more: one box of all blocks).  A page id out of
+    // range reads past the pool, which TMA fills with zeros.
+    auto tma_item = [&](const CUtensorMap* map, uint64_t* bar, uint32_t item, int blk0, int blocks,
+                        int x0, int page) {
+      const uint32_t full = bar_full(bar);
+      if (leader && lw == 0 && lane == 0)
+        mbar_arrive_expect_tx(bar, (uint32_t)(2 * blocks * kKBlk));
+      __syncwarp();
+      if (lw == 0) {
+        const int per = boxes == 1 ? 1 : blocks;
+        const int i = lane / per, blk = boxes == 1 ? 0 : lane % per;
+        if (lane < boxes * per) {
+          const int slot = slot_of(p, x0 + i * box, page, bad);
+          tma_load_3d_pair(item + blk * kKBlk + i * box * 128, map, full, 0,
+                           slot < 0 ? p.num_pages << p.page_shift : slot, blk0 + blk);
+        }
       }
+      __syncwarp();
+      if (lane == 0 && !(leader && lw == 0)) mbar_arrive_remote(full);
     };
-    auto copy_v = [&](const KeyTile& kt, int h, int s) {
-      const int mine =
-          lane < 16 ? lookup(kt, 64 * h + (lane >> 1) * 8 + lw * 2 + (lane & 1)) : -1;
-      const int ch = lane & 15;
-      const uint8_t* base =
-          static_cast<const uint8_t*>(kt.chunk ? p.v : p.vp) + (int)rank * 256 + ch * 16;
-      const uint32_t dst0 = vring_u + s * kVItem + (ch >> 3) * kKBlk;
-#pragma unroll
-      for (int it = 0; it < 8; ++it) {
-        const int r = __shfl_sync(0xffffffffu, mine, it * 2 + (lane >> 4));
-        const int row = it * 8 + lw * 2 + (lane >> 4);
-        cp_async16(dst0 + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
-                   base + ((long long)max(r, 0) * p.Hkv + x.g) * (kD * 2), r >= 0);
-      }
-    };
+    const uint32_t pitch = (uint32_t)p.Hkv * (kD * 2);             // bf16 rows
+    if (warp < 10) {
+      const uint32_t kring_u = smem_u32(kring), sQ_u = smem_u32(sQ);
+      const int my_row = 64 * (int)rank + (kE4M3 ? row16 : row32);
+      const int tma_row = 64 * (int)rank + (boxes == 1 ? 0 : min(lane >> 2, boxes - 1) * box);
+      uint32_t uk = 0, nq = 0;
+      int page = kNoRow;
+      auto copy_k = [&](const KeyTile& kt, uint32_t item) {
+        const int at = kt.tile * kBN;
+        const int mine = kt.chunk ? chunk_row(p, *px, codes, at + 64 * (int)rank + row32)
+                                  : slot_of(p, at + my_row, page, bad);
+        const uint8_t* base =
+            static_cast<const uint8_t*>(kt.chunk ? p.k : p.kp) + (px->g * (kD * 2) + lane * 16);
+        copy_rows(mine, base, pitch, item + (lane >> 3) * kKBlk, 32, lw, 2, 0, 1);
+      };
+      // e4m3: the next tile's raw rows wait in registers, 16 lanes per row.
+      uint4 raw[kE4M3 ? 16 : 1];
+      uint32_t ex = kNoExp;                    // of the row this lane looked up
+      auto fetch = [&](int idx) {
+        if constexpr (kE4M3) {
+          if (idx >= px->it0 + px->n) return;
+          const KeyTile kt = key_tile(*px, idx);
+          if (kt.chunk) return;
+          const int mine = slot_of(p, kt.tile * kBN + my_row, page, bad);
+          page = peek(idx + 1, my_row, 0);
+          ex = row_exp(p, p.ke, mine, px->g);
+          fetch_rows<16>(p, p.kp, piece16 * 16, px->g, raw,
+                         [&](int it) { return __shfl_sync(0xffffffffu, mine, it * 2 + sub16); });
 
-    // e4m3: raw rows in registers, a tile ahead of their use.  K: 16 lanes per
-    // row, rows it * 8 + lw * 2 + lane / 16; V half: 8 lanes per row, rows
-    // it * 16 + lw * 4 + lane / 8.
-    uint4 rk[kE4M3 ? 8 : 1], rv[2][kE4M3 ? 4 : 1];
-    uint32_t ek[kE4M3 ? 8 : 1], ev[2][kE4M3 ? 4 : 1];
-    auto fetch_k = [&](int idx) {
-      if constexpr (kE4M3) {
-        const KeyTile kt = key_tile(x, idx);
-        if (idx >= x.it0 + x.n || kt.chunk) return;
-        const int mine =
-            lane < 16 ? lookup(kt, 64 * (int)rank + (lane >> 1) * 8 + lw * 2 + (lane & 1)) : -1;
-#pragma unroll
-        for (int it = 0; it < 8; ++it) {
-          const int r = __shfl_sync(0xffffffffu, mine, it * 2 + (lane >> 4));
-          const long long at = (long long)r * p.Hkv + x.g;
-          rk[it] = make_uint4(0u, 0u, 0u, 0u);
-          ek[it] = 127u;
-          if (r >= 0) {
-            rk[it] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.kp) + at * kD +
-                                                     (lane & 15) * 16);
-            ek[it] = p.ke[at];
+        }
+      };
+      while ((px = next_segment()) != nullptr) {
+        const int i0 = px->it0, n = px->n;
+        if (n == 0) continue;
+        page = peek(i0, my_row, tma_row);
+        fetch(i0);
+        // Q: 32 lanes per row; rows past the unit's last token are zeros.
+        ok = acquire(&sm.q_empty, nq);
+        ++nq;
+        if (!ok) continue;
+        {
+          const uint8_t* qb = static_cast<const uint8_t*>(p.q) + lane * 16 +
+                              ((long long)px->b * p.Sq * p.Hq + (long long)px->g * p.G) * (kD * 2);
+          const uint32_t dst = sQ_u + (lane >> 3) * kQBlk;
+#pragma unroll 4
+          for (int it = 0; it < 64; ++it) {
+            const int r = it * 2 + lw;
+            const int row = (int)rank * kBM + r;
+            const int tok = px->tq0 + (row >> p.g_shift);
+            const int at = min(tok, px->tq1) * p.Hq + (row & (p.G - 1));
+            cp_async16(dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
+                       qb + (long long)at * (kD * 2), tok <= px->tq1);
+          }
+          push(bar_full(&sm.q_full));
+        }
+        for (int idx = i0; idx < i0 + n; ++idx) {
+          const KeyTile kt = key_tile(*px, idx);
+          const int s = (int)(uk % kNK);
+          const uint32_t item = kring_u + s * kKItem;
+          ok = acquire(&sm.k_empty[s], uk / kNK);
+          if (!ok) break;
+          ++uk;
+          const uint32_t full = bar_full(&sm.k_full[s]);
+          if (!kE4M3 && p.use_tma && whole_tile(p, *px, kt)) {
+            tma_item(&p.map_k, &sm.k_full[s], item, 4 * px->g, 4, kt.tile * kBN + 64 * (int)rank, page);
+            page = peek(idx + 1, my_row, tma_row);
+            if (n_pend > 0) flush();           // Q
+          } else if (!kE4M3 || kt.chunk) {
+            copy_k(kt, item);
+            if (!kE4M3) page = peek(idx + 1, my_row, tma_row);
+            push(full);
+            if (kE4M3 || idx == i0) flush();   // the first tile is waited for
+          } else {
+            if constexpr (kE4M3)
+              put_rows<16>(item, lw * 2 + sub16, 4, piece16, sub16, 2, raw, ex);
+            signal(full);
+            if (n_pend > 0) flush();           // Q
+          }
+          fetch(idx + 1);
+        }
+        flush();
+      }
+      land(sm.k_full, kNK, uk);
+    } else {
+      const uint32_t vring_u = smem_u32(vring);
+      const int my_row = kE4M3 ? row8 : row16;
+      const int tma_row = boxes == 1 ? 0 : min(lane >> 1, boxes - 1) * box;
+      uint32_t uv = 0;
+      int page0 = kNoRow, page1 = kNoRow;
+      auto copy_v = [&](const KeyTile& kt, int h, uint32_t item) {
+        const int at = kt.tile * kBN + 64 * h;
+        const int mine = kt.chunk ? chunk_row(p, *px, codes, at + row16)
+                                  : slot_of(p, at + my_row, h ? page1 : page0, bad);
+        const int ch = lane & 15;
+        const uint8_t* base = static_cast<const uint8_t*>(kt.chunk ? p.v : p.vp) +
+                              (px->g * (kD * 2) + (int)rank * 256 + ch * 16);
+        copy_rows(mine, base, pitch, item + (ch >> 3) * kKBlk, 16, lw * 2 + (lane >> 4), 4,
+                  lane >> 4, 2);
+      };
+      uint4 raw[2][kE4M3 ? 8 : 1];
+      uint32_t ex[2] = {kNoExp, kNoExp};
+      auto fetch = [&](int idx, int h) {
+        if constexpr (kE4M3) {
+          if (idx >= px->it0 + px->n) return;
+          const KeyTile kt = key_tile(*px, idx);
+          if (kt.chunk) return;
+          const int mine = slot_of(p, kt.tile * kBN + 64 * h + my_row, h ? page1 : page0, bad);
+          (h ? page1 : page0) = peek(idx + 1, 64 * h + my_row, 0);
+          ex[h] = row_exp(p, p.ve, mine, px->g);
+          fetch_rows<8>(p, p.vp, (int)rank * 128 + piece8 * 16, px->g, raw[h],
+                        [&](int it) { return __shfl_sync(0xffffffffu, mine, it * 4 + sub8); });
+
+        }
+      };
+      while ((px = next_segment()) != nullptr) {
+        const int i0 = px->it0, n = px->n;
+        if (n == 0) continue;
+        page0 = peek(i0, my_row, tma_row);
+        page1 = peek(i0, 64 + my_row, 64 + tma_row);
+        fetch(i0, 0);
+        fetch(i0, 1);
+        for (int idx = i0; idx < i0 + n && ok; ++idx) {
+          const KeyTile kt = key_tile(*px, idx);
+#pragma unroll(kE4M3 ? 2 : 1)
+          for (int h = 0; h < 2; ++h) {
+            const int s = (int)(uv % kNV);
+            const uint32_t item = vring_u + s * kVItem;
+            ok = ok && acquire(&sm.v_empty[s], uv / kNV);
+            if (!ok) break;
+            ++uv;
+            const uint32_t full = bar_full(&sm.v_full[s]);
+            if (!kE4M3) {
+              const bool tma = p.use_tma && whole_tile(p, *px, kt);
+              if (tma)
+                tma_item(&p.map_v, &sm.v_full[s], item, 4 * px->g + 2 * (int)rank, 2,
+                         kt.tile * kBN + 64 * h, h ? page1 : page0);
+              else
+                copy_v(kt, h, item);
+              const int next = peek(idx + 1, 64 * h + my_row, 64 * h + tma_row);
+              page0 = h ? page0 : next;
+              page1 = h ? next : page1;
+              if (!tma) push(full);
+            } else if (kt.chunk) {
+              copy_v(kt, h, item);
+              push(full);
+            } else {
+              if constexpr (kE4M3)
+                put_rows<8>(item, lw * 4 + sub8, 8, piece8, sub8, 4, raw[h], ex[h]);
+              signal(full);
+            }
+            fetch(idx + 1, h);
           }
         }
+        flush();
       }
-    };
-    auto fetch_v = [&](int idx, int h) {
-      if constexpr (kE4M3) {
-        const KeyTile kt = key_tile(x, idx);
-        if (idx >= x.it0 + x.n || kt.chunk) return;
-        const int mine =
-            lane < 16 ? lookup(kt, 64 * h + (lane >> 2) * 16 + lw * 4 + (lane & 3)) : -1;
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          const int r = __shfl_sync(0xffffffffu, mine, it * 4 + (lane >> 3));
-          const long long at = (long long)r * p.Hkv + x.g;
-          rv[h][it] = make_uint4(0u, 0u, 0u, 0u);
-          ev[h][it] = 127u;
-          if (r >= 0) {
-            rv[h][it] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.vp) +
-                                                        at * kD + (int)rank * 128 + (lane & 7) * 16);
-            ev[h][it] = p.ve[at];
-          }
-        }
-      }
-    };
-    // 16 raw bytes -> two 16-byte chunks; odd column blocks store them in the
-    // other order, so that the eight lanes of a store hit eight bank groups.
-    auto put16 = [&](uint32_t dst_row, int row, int c16, const uint4& w, uint32_t e) {
-      const float sc = exp_scale(e);
-      const float2 s2 = make_float2(sc, sc);
-      uint32_t a[4], b[4];
-      dequant8(w.x, w.y, s2, a);
-      dequant8(w.z, w.w, s2, b);
-      const bool swap = (c16 >> 2) & 1;
-      const int c = (c16 & 3) * 2;
-      const uint32_t base = dst_row + (c16 >> 2) * kKBlk;
-      const uint32_t d0 = base + (((c + (swap ? 1 : 0)) ^ (row & 7)) << 4);
-      const uint32_t d1 = base + (((c + (swap ? 0 : 1)) ^ (row & 7)) << 4);
-      st_shared_v4(d0, swap ? make_uint4(b[0], b[1], b[2], b[3]) : make_uint4(a[0], a[1], a[2], a[3]));
-      st_shared_v4(d1, swap ? make_uint4(a[0], a[1], a[2], a[3]) : make_uint4(b[0], b[1], b[2], b[3]));
-    };
-
-    auto load_k = [&](int idx) -> bool {
-      const KeyTile kt = key_tile(x, idx);
-      const int s = (int)(uk % kNK);
-      if (!acquire(&sm.k_empty[s], uk / kNK)) return false;
-      ++uk;
-      if (!kE4M3 || kt.chunk) {
-        copy_k(kt, s);
-        push(bar_full(&sm.k_full[s]));
-      } else {
-#pragma unroll
-        for (int it = 0; it < (kE4M3 ? 8 : 0); ++it) {
-          const int row = it * 8 + lw * 2 + (lane >> 4);
-          put16(kring_u + s * kKItem + row * 128, row, lane & 15, rk[it], ek[it]);
-        }
-        signal(bar_full(&sm.k_full[s]));
-        if (n_pend > 0) flush();              // Q, or a chunk tile's item
-      }
-      fetch_k(idx + 1);
-      return true;
-    };
-    auto load_v = [&](int idx, int h) -> bool {
-      const KeyTile kt = key_tile(x, idx);
-      const int s = (int)(uv % kNV);
-      if (!acquire(&sm.v_empty[s], uv / kNV)) return false;
-      ++uv;
-      if (!kE4M3 || kt.chunk) {
-        copy_v(kt, h, s);
-        push(bar_full(&sm.v_full[s]));
-      } else {
-#pragma unroll
-        for (int it = 0; it < (kE4M3 ? 4 : 0); ++it) {
-          const int row = it * 16 + lw * 4 + (lane >> 3);
-          put16(vring_u + s * kVItem + row * 128, row, lane & 7, rv[h][it], ev[h][it]);
-        }
-        signal(bar_full(&sm.v_full[s]));
-      }
-      return true;
-    };
-
-    while (next_segment(x)) {
-      if (!ok || x.n == 0) continue;
-      const int i0 = x.it0, n = x.n;
-      fetch_k(i0);
-      fetch_v(i0, 0);
-      fetch_v(i0, 1);
-      // Q: rows r of this CTA, 32 lanes per row.
-      ok = acquire(&sm.q_empty, nq);
-      ++nq;
-      if (!ok) continue;
-      {
-        const uint8_t* qb = static_cast<const uint8_t*>(p.q) + lane * 16;
-#pragma unroll 8
-        for (int it = 0; it < 32; ++it) {
-          const int r = it * 4 + lw;
-          const int row = (int)rank * kBM + r;
-          const int tok = x.tq0 + row / p.G;
-          const long long at = ((long long)x.b * p.Sq + min(tok, x.tq1)) * p.Hq +
-                               (long long)x.g * p.G + row % p.G;
-          cp_async16(sQ_u + (lane >> 3) * kQBlk + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
-                     qb + at * (kD * 2), tok <= x.tq1);
-        }
-        push(bar_full(&sm.q_full));
-      }
-      ok = load_k(i0);
-      if (ok && n > 1) ok = load_k(i0 + 1);
-      for (int j = 0; j < n && ok; ++j) {
-        if (j + 2 < n) ok = load_k(i0 + j + 2);
-        if (ok) ok = load_v(i0 + j, 0);
-        fetch_v(i0 + j + 1, 0);
-        if (ok) ok = load_v(i0 + j, 1);
-        fetch_v(i0 + j + 1, 1);
-      }
-      flush();
+      land(sm.v_full, kNV, uv);
     }
-    flush();
     if (bad) record_status(ctl, kStatusArg);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
     // ---------------------------------------------- softmax and epilogue
-    const int r = warp * 32 + lane;                // row of this thread in the CTA
-    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const int quarter = warp & 3, half = warp >> 2;
+    const int r = quarter * 32 + lane;             // row of this thread in the CTA
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t tSr = tS + lane_off + 64 * half, tOr = tO + lane_off + 128 * half;
     const float c = p.scale_log2;
     const uint32_t s_free_l0 = mapa_shared(smem_u32(&sm.s_free[0]), 0);
     const uint32_t s_free_l1 = mapa_shared(smem_u32(&sm.s_free[1]), 0);
     const uint32_t p_full_l = mapa_shared(smem_u32(&sm.p_full), 0);
     const uint32_t o_free_l = mapa_shared(smem_u32(&sm.o_free), 0);
-    uint8_t* const p_row0 = sP + r * 128;
-    uint8_t* const p_row1 = sP + kPBlk + r * 128;
-    uint32_t gt = 0;
+    uint8_t* const p_row = sP + half * kPBlk + r * 128;   // this thread's line of P
+    uint8_t* const st = sP + half * kPBlk + quarter * 4096;   // this warp's 32 lines
+    uint32_t gt = 0, n_pair = 0;
+    // Meets the quarter's other warp; what either wrote before is visible after.
+    auto pair_sync = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.pair[quarter]);
+      return warp_wait(&sm.pair[quarter], n_pair++ & 1, sm, ctl);
+    };
 
-    while (next_segment(x)) {
-      if (!ok) continue;
+    while (const Segment* px = next_segment()) {
+      const Segment& x = *px;
       const int row = (int)rank * kBM + r;         // row of the query tile
-      const int tok_raw = x.tq0 + row / p.G;
+      const int tok_raw = x.tq0 + (row >> p.g_shift);
       const bool row_valid = tok_raw <= x.tq1;
       const int tok = min(tok_raw, x.tq1);
       const long long orow =
-          ((long long)x.b * p.Sq + tok) * p.Hq + (long long)x.g * p.G + row % p.G;
+          ((long long)x.b * p.Sq + tok) * p.Hq + (long long)x.g * p.G + (row & (p.G - 1));
       float* po = nullptr;
       float* pml = nullptr;
       if (x.slot >= 0) {
         const long long at = (long long)x.slot * kRowsTile + row;
-        po = p.ws + at * kD;
+        po = p.ws + at * kD + 128 * half;
         pml = p.ws + (long long)p.n_clusters * 2 * kRowsTile * kD + at * 2;
       }
       if (x.n == 0) {
         if (pml != nullptr) {
-          if (row_valid) *reinterpret_cast<float2*>(pml) = make_float2(-INFINITY, 0.f);
+          if (row_valid && half == 0) *reinterpret_cast<float2*>(pml) = make_float2(-INFINITY, 0.f);
         } else {                                   // a whole unit without a key: zeros
-          for (int rr = 0; rr < 32; ++rr) {
+          for (int rr = 16 * half; rr < 16 * half + 16; ++rr) {
             const long long at = __shfl_sync(0xffffffffu, orow, rr);
             const bool v = __shfl_sync(0xffffffffu, (int)row_valid, rr) != 0;
             if (v)
               *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + at * (kD * 2) + lane * 16) =
                   make_uint4(0u, 0u, 0u, 0u);
           }
-          if (p.lse && row_valid) p.lse[orow] = -INFINITY;
+          if (p.lse && row_valid && half == 0) p.lse[orow] = -INFINITY;
         }
         continue;
       }
       const uint32_t cq = codes[tok];
-      const uint32_t csq = cq >> 2;
-      const bool row_expert = (cq & 2u) != 0;
       const bool row_pad = is_pad(cq);
-      const int lo = window_lo(p, x.len, tok);     // cached keys below it: sinks only
-      const int sink_end = p.window > 0 ? min(p.sinks, x.len) : 0;
-      float m_run = -INFINITY, l_run = 0.f;
+      const bool any_pad = __any_sync(0xffffffffu, row_pad);
+      float m_run = -INFINITY, l_run = 0.f;        // l: this thread's half of the keys
 
       for (int li = 0; li < x.n; ++li, ++gt) {
         const int bs = (int)(gt & 1);
@@ -828,89 +1121,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int k0 = kt.tile * kBN;
         // Does every row of the unit see every key of the tile?
         bool partial;
-        uint32_t fl = 0;
         if (kt.chunk) {
-          fl = sm.tile_fast[kt.tile];
+          const uint32_t fl = sm.tile_fast[kt.tile];
           partial = k0 + kBN > p.Sq || sm.tile_cs_last[kt.tile] > x.csq0 || (fl & 4u) ||
                     (x.any_e && (fl & 1u)) ||
                     (p.window > 0 && x.tq1 - k0 >= p.window && x.len + k0 + kBN > p.sinks);
         } else {
           partial = k0 + kBN > x.len || (p.window > 0 && k0 < x.lo1 && k0 + kBN > p.sinks);
         }
+        uint2 vis = make_uint2(~0u, ~0u);
+        if (partial) vis = row_mask(p, codes, x, kt.chunk, k0 + 64 * half, tok, cq);
+        if (row_pad) vis = make_uint2(0u, 0u);
         if (!warp_wait(&sm.s_full[bs], (gt >> 1) & 1, sm, ctl)) { ok = false; break; }
         tc_fence_after();
-        float xs[kBN];
+        float xs[64];
         {
-          uint32_t r0[32], r1[32], r2[32], r3[32];
-          tmem_ld32(tS + lane_off + 128 * bs, r0);
-          tmem_ld32(tS + lane_off + 128 * bs + 32, r1);
-          tmem_ld32(tS + lane_off + 128 * bs + 64, r2);
-          tmem_ld32(tS + lane_off + 128 * bs + 96, r3);
+          uint32_t r0[32], r1[32];
+          tmem_ld32(tSr + 128 * bs, r0);
+          tmem_ld32(tSr + 128 * bs + 32, r1);
           tmem_ld_wait();
           reg_fence(r0);
           reg_fence(r1);
-          reg_fence(r2);
-          reg_fence(r3);
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             xs[e] = __uint_as_float(r0[e]);
             xs[32 + e] = __uint_as_float(r1[e]);
-            xs[64 + e] = __uint_as_float(r2[e]);
-            xs[96 + e] = __uint_as_float(r3[e]);
           }
         }
-        // S is in registers: the next QK into this buffer may start.
+        if (partial || any_pad) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            xs[e] = ((vis.x >> e) & 1u) ? xs[e] : -INFINITY;
+            xs[32 + e] = ((vis.y >> e) & 1u) ? xs[32 + e] : -INFINITY;
+          }
+        }
+        float m4[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float a = xs[k];
+#pragma unroll
+          for (int i = 1; i < 15; i += 2) a = fmax3(a, xs[k + 4 * i], xs[k + 4 * i + 4]);
+          m4[k] = fmaxf(a, xs[k + 60]);
+        }
+        // The row's maximum over both halves: each thread leaves its own in the
+        // first column of its half of S, which only it reads.
+        float mx = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * c;
+        tmem_st1(tSr + 128 * bs, __float_as_uint(mx));
+        tmem_st_wait();
+        tc_fence_before();
+        if (!pair_sync()) { ok = false; break; }
+        tc_fence_after();
+        {
+          uint32_t o[1];
+          tmem_ld1(tS + lane_off + 64 * (1 - half) + 128 * bs, o[0]);
+          tmem_ld_wait();
+          reg_fence(o);
+          mx = fmaxf(mx, __uint_as_float(o[0]));
+        }
+        // S has been read: the QK after next may overwrite it.
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(bs ? s_free_l1 : s_free_l0);
-        if (partial || __any_sync(0xffffffffu, row_pad)) {
-          // One visibility bit per key of the tile.
-          uint32_t vm[4] = {~0u, ~0u, ~0u, ~0u};
-          if (partial) {
-            // Visible keys, as offsets in the tile: [a, e) and [0, s).
-            int a, e, s;
-            if (kt.chunk) {
-              e = 0;                               // keys whose block the row admits: a prefix
-#pragma unroll
-              for (int step = kBN; step >= 1; step >>= 1) {
-                const int probe = e + step;
-                if (probe <= kBN && (uint32_t)(codes[k0 + probe - 1] >> 2) <= csq) e = probe;
-              }
-              e = min(e, p.Sq - k0);
-              a = p.window > 0 ? tok - p.window + 1 - k0 : 0;
-              s = p.window > 0 ? min(max(p.sinks - x.len, 0) - k0, e) : 0;
-#pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                // FAST bit (padding keys carry it too) and padding, per key
-                const uint32_t ck = codes[k0 + 32 * w + lane];
-                const uint32_t fw = __ballot_sync(0xffffffffu, (ck & 1u) != 0u);
-                const uint32_t pw = __ballot_sync(0xffffffffu, is_pad(ck));
-                vm[w] = ~(row_expert ? fw : pw);
-              }
-            } else {
-              e = min(kBN, x.len - k0);
-              a = lo - k0;
-              s = sink_end - k0;
-            }
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-              vm[w] &= (bits_below(e - 32 * w) & ~bits_below(a - 32 * w)) | bits_below(s - 32 * w);
-          }
-          if (row_pad) vm[0] = vm[1] = vm[2] = vm[3] = 0u;
-#pragma unroll
-          for (int j = 0; j < kBN; ++j) xs[j] = ((vm[j >> 5] >> (j & 31)) & 1u) ? xs[j] : -INFINITY;
-        }
-        float m8[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float a = fmax3(xs[k], xs[k + 8], xs[k + 16]);
-#pragma unroll
-          for (int i = 3; i < 15; i += 2) a = fmax3(a, xs[k + 8 * i], xs[k + 8 * i + 8]);
-          m8[k] = fmaxf(a, xs[k + 120]);
-        }
-        const float mx =
-            fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], fmax3(m8[4], m8[5], m8[6]), m8[7])) * c;
-        // Lazy rescaling (exact: O and l always share the reference maximum).
+        // Lazy rescaling.
         const bool upd = mx > m_run + kRescaleThreshold;
         const float m_new = upd ? mx : m_run;
         const float alpha = ex2(m_run - m_new);
@@ -921,9 +1193,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float2 c2 = make_float2(c, c), n2 = make_float2(nm, nm);
         float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                         make_float2(0.f, 0.f)};
-        uint32_t pk[64];
+        uint32_t pk[32];
 #pragma unroll
-        for (int e = 0; e < 64; ++e) {
+        for (int e = 0; e < 32; ++e) {
           const float2 t = ffma2(make_float2(xs[2 * e], xs[2 * e + 1]), c2, n2);
           const float2 pp = make_float2(ex2(t.x), ex2(t.y));
           ls[e & 3] = fadd2(ls[e & 3], pp);
@@ -941,24 +1213,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (rescale) {
           const float a = need_o ? alpha : 1.f;
 #pragma unroll 1
-          for (int cc = 0; cc < kD / 32; ++cc) {
+          for (int cc = 0; cc < 4; ++cc) {
             uint32_t o[32];
-            tmem_ld32(tO + lane_off + 32 * cc, o);
+            tmem_ld32(tOr + 32 * cc, o);
             tmem_ld_wait();
             reg_fence(o);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-            tmem_st32(tO + lane_off + 32 * cc, o);
+            tmem_st32(tOr + 32 * cc, o);
           }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int sw = (j ^ (r & 7)) << 4;
-          *reinterpret_cast<uint4*>(p_row0 + sw) =
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(p_row + ((j ^ (r & 7)) << 4)) =
               make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
-          *reinterpret_cast<uint4*>(p_row1 + sw) =
-              make_uint4(pk[32 + 4 * j], pk[33 + 4 * j], pk[34 + 4 * j], pk[35 + 4 * j]);
-        }
         fence_proxy_async_smem();
         if (rescale) tmem_st_wait();
         tc_fence_before();
@@ -970,62 +1238,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ----------------------------------------------------- epilogue
       if (!warp_wait(&sm.o_done, (gt - 1) & 1, sm, ctl)) { ok = false; continue; }
       tc_fence_after();
+      // The row's other half of l, through the P line (free: the last PV is done).
+      float l_all;
+      {
+        float* const mine = reinterpret_cast<float*>(p_row);
+        const float* const other = reinterpret_cast<const float*>(sP + (1 - half) * kPBlk + r * 128);
+        *mine = l_run;
+        if (!pair_sync()) { ok = false; continue; }   // both halves have written
+        l_all = l_run + *other;
+        if (!pair_sync()) { ok = false; continue; }   // and read: the lines are free
+      }
       if (po == nullptr) {
-        const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-        // P is free: each warp stages its 32 rows there, 128 columns (256
-        // bytes) at a time, then writes whole half rows.
-        // (A warp stays inside its own P rows: another warp may already write
-        // the next segment's P.)
-        uint8_t* const st = sP + warp * 4096;
-        auto staged = [&](int rr, int ch) {        // row rr's 16-byte chunk ch
-          return reinterpret_cast<uint4*>(st + (ch >> 3) * kPBlk + rr * 128 +
-                                          (((ch & 7) ^ (rr & 7)) << 4));
-        };
+        const float inv = l_all > 0.f ? 1.f / l_all : 0.f;
+        // Each warp stages 32 rows of 64 columns in its own P lines (another
+        // warp may already write the next segment's P), then writes row pieces
+        // of 128 bytes.
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
+        for (int sub = 0; sub < 2; ++sub) {
+          uint32_t o0[32], o1[32];
+          tmem_ld32(tOr + 64 * sub, o0);
+          tmem_ld32(tOr + 64 * sub + 32, o1);
+          tmem_ld_wait();
+          reg_fence(o0);
+          reg_fence(o1);
 #pragma unroll
-          for (int sub = 0; sub < 4; ++sub) {
-            uint32_t o[32];
-            tmem_ld32(tO + lane_off + 128 * half + 32 * sub, o);
-            tmem_ld_wait();
-            reg_fence(o);
+          for (int j = 0; j < 8; ++j) {
+            uint32_t w[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = cvt_bf16x2(__uint_as_float(o[8 * j + 2 * e]) * inv,
-                                  __uint_as_float(o[8 * j + 2 * e + 1]) * inv);
-              *staged(lane, 4 * sub + j) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < 4; ++e) {
+              const int at = 8 * j + 2 * e;
+              const uint32_t lo_w = at < 32 ? o0[at & 31] : o1[at & 31];
+              const uint32_t hi_w = at < 32 ? o0[(at + 1) & 31] : o1[(at + 1) & 31];
+              w[e] = cvt_bf16x2(__uint_as_float(lo_w) * inv, __uint_as_float(hi_w) * inv);
+              if (l_all == 0.f) w[e] = 0u;         // O may hold 0 * inf of other rows' keys
             }
+            *reinterpret_cast<uint4*>(st + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
-          if (half == 1) {                         // O has been read
+          if (sub == 1) {                          // this warp's part of O has been read
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(o_free_l);
           }
           __syncwarp();
-#pragma unroll 4
-          for (int it = 0; it < 16; ++it) {
-            const int rr = it * 2 + (lane >> 4), ch = lane & 15;
+#pragma unroll
+          for (int it = 0; it < 8; ++it) {
+            const int rr = it * 4 + (lane >> 3), ch = lane & 7;
             const long long at = __shfl_sync(0xffffffffu, orow, rr);
             const bool v = __shfl_sync(0xffffffffu, (int)row_valid, rr) != 0;
-            const uint4 w = *staged(rr, ch);
+            const uint4 w = *reinterpret_cast<const uint4*>(st + rr * 128 + ((ch ^ (rr & 7)) << 4));
             if (v)
               *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + at * (kD * 2) + half * 256 +
-                                        ch * 16) = w;
+                                        sub * 128 + ch * 16) = w;
           }
           __syncwarp();
         }
-        if (p.lse && row_valid)
-          p.lse[orow] = l_run > 0.f ? (m_run + __log2f(l_run)) * 0.69314718055994531f
-                                    : (l_run == l_run ? -INFINITY : l_run);
+        if (p.lse && row_valid && half == 0)
+          p.lse[orow] = l_all > 0.f ? (m_run + __log2f(l_all)) * 0.69314718055994531f
+                                    : (l_all == l_all ? -INFINITY : l_all);
       } else {
         // Partial: unnormalised O and (m, l).
 #pragma unroll 1
-        for (int cc = 0; cc < kD / 32; ++cc) {
+        for (int cc = 0; cc < 4; ++cc) {
           uint32_t o[32];
-          tmem_ld32(tO + lane_off + 32 * cc, o);
+          tmem_ld32(tOr + 32 * cc, o);
           tmem_ld_wait();
           reg_fence(o);
           if (row_valid) {
@@ -1038,7 +1314,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(o_free_l);
-        if (row_valid) *reinterpret_cast<float2*>(pml) = make_float2(m_run, l_run);
+        if (row_valid && half == 0) *reinterpret_cast<float2*>(pml) = make_float2(m_run, l_all);
       }
     }
   }
@@ -1049,7 +1325,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync();
-  if (warp == 8) {
+  if (warp == 12) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
@@ -1059,23 +1335,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // sum_k 2^(m_k - M) l_k with M the largest m_k that has l_k > 0.  CTA (u, y):
 // rows [32 y, 32 y + 32) of unit u, one warp per row at a time, 8 columns per
 // lane.  HBM-bound: reads the fp32 partials once.
-struct CombineSmem {
-  long long cum[kGroup + 1];
-  int max_nom;
-};
 __global__ void __launch_bounds__(256)
     paged_combine_kernel(const __grid_constant__ PagedTcParams p, const DevCtl ctl) {
-  __shared__ CombineSmem sm;
+  __shared__ Plan plan;
   pdl_wait();                  // the partials come from the kernel before
   pdl_launch_dependents();
-  build_schedule<256>(p, ctl, sm.cum, &sm.max_nom);
-  const long long per = tiles_per_cluster(p, sm.cum[p.nb], sm.max_nom);
+  if (threadIdx.x < 32) make_plan(p, ctl, plan, threadIdx.x);
+  __syncthreads();
+  const int per = tiles_per_cluster(p, plan);
   if (per == 0) return;
   const int units = p.Hkv * p.n_tiles;
   const int b = (int)(blockIdx.x / units), u = (int)(blockIdx.x % units);
-  const int nom = (int)((sm.cum[b + 1] - sm.cum[b]) / units);
-  const long long t0 = sm.cum[b] + (long long)u * nom;
-  const int c0 = (int)(t0 / per), c1 = (int)((t0 + nom - 1) / per);
+  const int nom = (plan.cum[b + 1] - plan.cum[b]) / units;
+  const int t0 = plan.cum[b] + u * nom;
+  const int c0 = t0 / per, c1 = (t0 + nom - 1) / per;
   if (c0 == c1) return;        // ran whole
   const int g = u / p.n_tiles, tile = u % p.n_tiles;
   const int lane = threadIdx.x & 31;
@@ -1083,7 +1356,7 @@ __global__ void __launch_bounds__(256)
       p.ws + (long long)p.n_clusters * 2 * kRowsTile * kD);
   for (int i = threadIdx.x >> 5; i < 32; i += 8) {
     const int row = blockIdx.y * 32 + i;
-    const int tok = tile * p.tok_per_tile + row / p.G;
+    const int tok = tile * p.tok_per_tile + (row >> p.g_shift);
     if (tok >= p.Sq || row >= p.G * p.tok_per_tile) continue;
     float M = -INFINITY;
     for (int c = c0; c <= c1; ++c) {
@@ -1106,7 +1379,7 @@ __global__ void __launch_bounds__(256)
       acc[4] += w * d.x; acc[5] += w * d.y; acc[6] += w * d.z; acc[7] += w * d.w;
     }
     const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-    const long long orow = ((long long)(p.b0 + b) * p.Sq + tok) * p.Hq + (long long)g * p.G + row % p.G;
+    const long long orow = ((long long)(p.b0 + b) * p.Sq + tok) * p.Hq + (long long)g * p.G + (row & (p.G - 1));
     uint4 w;
     w.x = cvt_bf16x2(acc[0] * inv, acc[1] * inv);
     w.y = cvt_bf16x2(acc[2] * inv, acc[3] * inv);
@@ -1128,6 +1401,21 @@ cudaError_t launch(PagedTcParams& p, const DevCtl& ctl, cudaStream_t st) {
                     (size_t)p.smem_bytes, st, p, ctl);
 }
 
+// A pool [slots][Hkv][256] bf16 as (64, slots, 4 Hkv column blocks).
+bool encode_pool(CUtensorMap* map, const void* base, const PagedParams& p, uint32_t box_blocks) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const uint32_t rows = 1u << p.page_shift;
+  cuuint64_t dims[3] = {64, (cuuint64_t)p.num_pages << p.page_shift, 4 * (cuuint64_t)p.Hkv};
+  cuuint64_t strides[2] = {(cuuint64_t)p.Hkv * kD * 2, 128};
+  cuuint32_t box[3] = {64, rows < 64 ? rows : 64, rows < 64 ? 1 : box_blocks};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Whether a group of nb sequences may be cut: with four units or more per
 // cluster the last round's idle clusters cost less than partials and a merge.
 bool may_cut(long long n_units, int slots) { return n_units < 4ll * slots; }
@@ -1136,32 +1424,47 @@ int slots() { return max(sm_count() / 2, 1); }
 
 }  // namespace
 
+// Sequences per launch: at most kGroup, their tiles below 2^31.
+static int group_size(const PagedParams& p) {
+  const int G = p.Hq / p.Hkv;
+  const long long units = (long long)p.Hkv * ((p.Sq + kRowsTile / G - 1) / (kRowsTile / G));
+  const long long tiles = (((long long)p.max_pages << p.page_shift) + kBN - 1) / kBN +
+                          (p.Sq + kBN - 1) / kBN;
+  const long long n = ((1ll << 31) - 1) / max(units * tiles, 1ll);
+  return (int)min(n, (long long)kGroup);
+}
+
 bool paged_tc_applies(const PagedParams& p) {
   const int G = p.Hq / p.Hkv;
   return !p.f32 && p.d == kD && (G == 1 || G == 2 || G == 4 || G == 8 || G == 16) &&
-         (long long)p.B * p.Sq < (1ll << 31);
+         (long long)p.B * p.Sq < (1ll << 31) && group_size(p) >= 1;
 }
 
 size_t paged_tc_workspace_bytes(const PagedParams& p) {
-  const int G = p.Hq / p.Hkv;
+  const int G = p.Hq / p.Hkv, group = group_size(p);
   const long long units = (long long)p.Hkv * ((p.Sq + kRowsTile / G - 1) / (kRowsTile / G));
   // The last group of sequences is the smallest: it decides.
-  const int last = p.B % kGroup ? p.B % kGroup : kGroup;
-  if (!may_cut((p.B < kGroup ? p.B : last) * units, slots())) return 0;
+  const int last = p.B % group ? p.B % group : group;
+  if (!may_cut(last * units, slots())) return 0;
   return (size_t)slots() * 2 * kRowsTile * (kD + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_tc(const PagedParams& a, float* ws, const DevCtl& ctl, cudaStream_t st) {
-  PagedTcParams p;
+  PagedTcParams p{};
   static_cast<PagedParams&>(p) = a;
   p.ws = ws;
   p.G = a.Hq / a.Hkv;
+  p.g_shift = p.G == 1 ? 0 : p.G == 2 ? 1 : p.G == 4 ? 2 : p.G == 8 ? 3 : 4;
   p.tok_per_tile = kRowsTile / p.G;
   p.n_tiles = (a.Sq + p.tok_per_tile - 1) / p.tok_per_tile;
   p.scale_log2 = a.scale * 1.4426950408889634f;
-  for (int b0 = 0; b0 < a.B; b0 += kGroup) {
+  p.use_tma = a.cache_dtype == kCacheBF16 && a.num_pages > 0;
+  if (p.use_tma && (!encode_pool(&p.map_k, a.kp, a, 4) || !encode_pool(&p.map_v, a.vp, a, 2)))
+    return cudaErrorUnknown;
+  const int group = group_size(a);
+  for (int b0 = 0; b0 < a.B; b0 += group) {
     p.b0 = b0;
-    p.nb = min(kGroup, a.B - b0);
+    p.nb = min(group, a.B - b0);
     const long long n_units = (long long)p.nb * a.Hkv * p.n_tiles;
     p.may_cut = may_cut(n_units, slots()) ? 1 : 0;
     p.n_clusters = p.may_cut ? slots() : (int)min(n_units, (long long)slots());
