@@ -83,6 +83,16 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// The same with a shared-memory address.
+__device__ __forceinline__ void tma_load_3d_at(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
+                                               int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
 // 4-D tiled load: one instruction brings a whole [rows x 4 x 64] operand tile,
 // landing as 4 column blocks of [rows x 64] (dimension 2 walks the blocks).
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,

@@ -43,6 +43,50 @@ __device__ __forceinline__ float exp_scale(uint32_t byte) {
                    : byte == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte << 23);
 }
 
+// Four raw e4m3 -> two bf16x2 words, times 2^(byte - 127), exact.  The byte's
+// exponent and mantissa moved to bf16's places read as the value times 2^-120
+// (subnormals too); the multiplication by m = 2^(byte - 7) undoes that and applies
+// the scale.  Integer and fp16-pipe instructions only: the conversion
+// instructions run at a quarter of their rate, on the units that the softmax's
+// exponentials need (7600 cycles a tile with them, 3 times the MMAs' time).
+__device__ __forceinline__ uint2 dequant4(uint32_t w, uint32_t m) {
+  uint2 o;
+  const uint32_t x0 = __byte_perm(w, 0u, 0x1404), x1 = __byte_perm(w, 0u, 0x3424);
+  const uint32_t y0 = ((x0 >> 4) & 0x07f007f0u) | (x0 & 0x80008000u);
+  const uint32_t y1 = ((x1 >> 4) & 0x07f007f0u) | (x1 & 0x80008000u);
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.x) : "r"(y0), "r"(m));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.y) : "r"(y1), "r"(m));
+  return o;
+}
+// bf16x2 of 2^(byte - 7) twice (at most 2^127: rest_scale has what is missing);
+// NaN for byte 255, 0 where there is no row.
+constexpr uint32_t kNoExp = 256u;
+__device__ __forceinline__ uint32_t main_scale(uint32_t byte) {
+  const uint32_t f = byte == kNoExp ? 0u : byte == 255u ? 0x7FC0u : min(byte + 120u, 254u) << 7;
+  return f * 0x10001u;
+}
+// Scales above 2^7 (values above 448 * 2^7): bf16x2 of 2^(byte - 134).
+__device__ __forceinline__ uint32_t rest_scale(uint32_t byte) {
+  return ((byte >= 255u || byte <= 134u ? 127u : byte - 7u) << 7) * 0x10001u;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t o;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(a), "r"(b));
+  return o;
+}
+
+// The same for a transposed pair: bytes (key 0: d 0, d 1; key 1: d 0, d 1) ->
+// words (key 0, key 1) of d 0 and of d 1, times m's halves for the two keys.
+__device__ __forceinline__ uint2 dequant4_t(uint32_t w, uint32_t m) {
+  uint2 o;
+  const uint32_t x0 = __byte_perm(w, 0u, 0x2404), x1 = __byte_perm(w, 0u, 0x3414);
+  const uint32_t y0 = ((x0 >> 4) & 0x07f007f0u) | (x0 & 0x80008000u);
+  const uint32_t y1 = ((x1 >> 4) & 0x07f007f0u) | (x1 & 0x80008000u);
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.x) : "r"(y0), "r"(m));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.y) : "r"(y1), "r"(m));
+  return o;
+}
+
 // Writing to and reading from the pages (cache.cu).
 constexpr int kCacheMaxTok = 128;    // tokens per CTA at most
 struct CacheParams {
@@ -145,6 +189,22 @@ struct PagedTcParams : PagedParams {
 bool paged_tc_applies(const PagedParams& p);
 size_t paged_tc_workspace_bytes(const PagedParams& p);
 cudaError_t launch_paged_tc(const PagedParams& p, float* ws, const DevCtl& ctl, cudaStream_t st);
+
+// At most 8 query rows per kv head: bf16 queries, d = 256, G in {1, 2, 4, 8}
+// (paged_decode.cu).
+constexpr int kPagedDecodeGroup = 128;
+struct PagedDecodeParams : PagedParams {
+  CUtensorMap map_k, map_v;  // the pools, boxes of 16 rows
+  float* ws;                 // partials [n_ctas * 2][8 rows][256], then (m, l)
+  int G, g_shift;
+  int b0, nb;                // this launch's sequences
+  int n_ctas;
+  float scale_log2;
+};
+bool paged_decode_applies(const PagedParams& p);
+size_t paged_decode_workspace_bytes(const PagedParams& p);
+cudaError_t launch_paged_decode(const PagedParams& p, float* ws, const DevCtl& ctl,
+                                cudaStream_t st);
 
 cudaError_t launch_paged_simt(const PagedParams& p, const DevCtl& ctl, cudaStream_t st);
 

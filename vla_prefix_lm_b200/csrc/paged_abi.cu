@@ -172,6 +172,7 @@ int pi_attn_cache_read(const pi_paged_desc* d, const void* k_pages, const void* 
 size_t pi_attn_paged_workspace_bytes(const pi_paged_desc* d) {
   if (check_attn(d) != PI_OK || d->B == 0 || d->Sq == 0) return 0;
   const PagedParams p = paged_params(d);
+  if (paged_decode_applies(p)) return paged_decode_workspace_bytes(p);
   return paged_tc_applies(p) ? paged_tc_workspace_bytes(p) : 0;
 }
 
@@ -204,8 +205,9 @@ int pi_attn_paged(const pi_paged_desc* d, const void* q, const void* k_new, cons
   p.ar = ar_mask; p.seg = segment_ids;
   p.out = out; p.lse = lse;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (paged_tc_applies(p))
-    return launched(launch_paged_tc(p, need > 0 ? static_cast<float*>(workspace) : nullptr, ctl, st));
+  float* ws = need > 0 ? static_cast<float*>(workspace) : nullptr;
+  if (paged_decode_applies(p)) return launched(launch_paged_decode(p, ws, ctl, st));
+  if (paged_tc_applies(p)) return launched(launch_paged_tc(p, ws, ctl, st));
   return launched(launch_paged_simt(p, ctl, st));
 }
 
