@@ -14,7 +14,6 @@ Names mirror the C ABI in include/pi_attn.h: ``pi_attn_prefill``,
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -462,52 +461,101 @@ def pi_euler_update(x, v, dt, stream=None):
 _CACHE_CODES = {torch.bfloat16: PI_BF16, torch.float32: PI_F32, torch.float8_e4m3fn: PI_E4M3}
 
 
-def _paged_desc(B, Sq, Hq, dtype, k_pages, v_pages, page_table, cache_lens, k_exp, v_exp,
-                window=0, sinks=0, softmax_scale=1.0, mask_stride=0):
-    """Checks the cache's tensors against each other and returns the descriptor."""
-    if dtype not in (torch.bfloat16, torch.float32):
+# Descriptors (and workspace sizes) by their values: building one costs more
+# than looking it up.
+_paged_descs = {}
+
+
+def _paged_desc(B, Sq, Hq, dtype, k_pages, page_table, window=0, sinks=0, softmax_scale=1.0,
+                mask_stride=0):
+    """(descriptor reference, workspace bytes) of a call."""
+    key = (B, Sq, Hq, dtype, k_pages.shape, k_pages.dtype, page_table.shape[1], window, sinks,
+           softmax_scale, mask_stride, torch.cuda.current_device())
+    got = _paged_descs.get(key)
+    if got is None:
+        n, page, Hkv, d = k_pages.shape
+        desc = PiPagedDesc(B, Sq, Hq, Hkv, d, PI_BF16 if dtype == torch.bfloat16 else PI_F32,
+                           _CACHE_CODES[k_pages.dtype], page, n, page_table.shape[1],
+                           int(window), int(sinks), float(softmax_scale), 0, mask_stride)
+        ref = ctypes.byref(desc)
+        got = (ref, int(lib().pi_attn_paged_workspace_bytes(ref)), desc)
+        if len(_paged_descs) >= 1024:
+            _paged_descs.clear()
+        _paged_descs[key] = got
+    return got
+
+
+def _check_cache(B, dtype, k_pages, v_pages, page_table, cache_lens, k_exp, v_exp):
+    """Checks the cache's tensors against each other (their device and
+    contiguity are checked with their addresses)."""
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise ValueError(f"unsupported dtype {dtype}")
-    _need(k_pages, "k_pages", dims=4)
-    _need(v_pages, "v_pages", k_pages.dtype, 4)
-    _need(page_table, "page_table", torch.int32, 2)
-    _need(cache_lens, "cache_lens", torch.int32, 1)
-    if k_pages.dtype not in _CACHE_CODES:
-        raise ValueError(f"unsupported cache dtype {k_pages.dtype}")
-    shape = k_pages.shape
-    if v_pages.shape != shape:
-        raise ValueError("v_pages must have k_pages' shape")
-    if page_table.shape[0] != B or cache_lens.shape[0] != B:
-        raise ValueError("page_table must be [B, max_pages] and cache_lens [B]")
-    if k_pages.dtype == torch.float8_e4m3fn:
-        _need(k_exp, "k_exp", torch.uint8, 3)
-        _need(v_exp, "v_exp", torch.uint8, 3)
-        if k_exp.shape != shape[:3] or v_exp.shape != shape[:3]:
-            raise ValueError("k_exp/v_exp must be [num_pages, page_size, Hkv]")
+    shape, cache = k_pages.shape, k_pages.dtype
+    if len(shape) != 4 or v_pages.shape != shape or v_pages.dtype is not cache:
+        raise ValueError("k_pages and v_pages must be [num_pages, page_size, Hkv, d] of one dtype")
+    if cache not in _CACHE_CODES:
+        raise ValueError(f"unsupported cache dtype {cache}")
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be int32 [B, max_pages]")
+    if cache_lens.dtype is not torch.int32 or cache_lens.shape != (B,):
+        raise ValueError("cache_lens must be int32 [B]")
+    if cache is torch.float8_e4m3fn:
+        for e in (k_exp, v_exp):
+            if e is None or e.dtype is not torch.uint8 or e.shape != shape[:3]:
+                raise ValueError("k_exp and v_exp must be uint8 [num_pages, page_size, Hkv]")
     elif k_exp is not None or v_exp is not None:
         raise ValueError("k_exp/v_exp belong to a float8_e4m3fn cache")
-    return PiPagedDesc(B, Sq, Hq, shape[2], shape[3],
-                       PI_BF16 if dtype == torch.bfloat16 else PI_F32,
-                       _CACHE_CODES[k_pages.dtype], shape[1], shape[0], page_table.shape[1],
-                       int(window), int(sinks), float(softmax_scale), 0, mask_stride)
 
 
-def _one_device(*tensors):
-    """The tensors' device; they must share it and it must be the current one
-    (kernels are launched there)."""
-    index = torch.cuda.current_device()
+def _like(t, name, shape, dtype):
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _addresses(*tensors):
+    """The tensors' addresses (None stays None).  They must be contiguous and on
+    the current device, where kernels are launched."""
+    index = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    got = []
     for t in tensors:
-        if t is not None and t.device.index != index:
-            raise ValueError(f"tensors must be on the current device, cuda:{index}; "
+        if t is None:
+            got.append(None)
+            continue
+        if t.get_device() != index:
+            raise ValueError(f"tensors must be CUDA tensors on the current device, cuda:{index}; "
                              f"got one on {t.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"tensors must be contiguous; got shape {tuple(t.shape)} with strides "
+                             f"{t.stride()}")
+        got.append(t.data_ptr())
+    return got
+
+
+# The current stream's handle without a Stream object around it (4 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _handle(stream):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return _stream(stream)
 
 
 def _on(stream):
     """A context in which tensors are allocated for use on ``stream``."""
-    if stream is None:
-        return contextlib.nullcontext()
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))
     return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, near, stream):
+    """A tensor on ``near``'s device, for use on ``stream``."""
+    if stream is not None:
+        with _on(stream):
+            return near.new_empty(shape, dtype=dtype)
+    if near.shape == shape and near.dtype is dtype:
+        return torch.empty_like(near)            # the cheapest form
+    return near.new_empty(shape, dtype=dtype)
 
 
 def pi_attn_cache_write(k_new, v_new, k_pages, v_pages, page_table, cache_lens, token_mask=None,
@@ -518,27 +566,23 @@ def pi_attn_cache_write(k_new, v_new, k_pages, v_pages, page_table, cache_lens, 
     [B,max_pages]; cache_lens int32 [B].  Valid tokens (``token_mask`` uint8
     [Sq] or [B,Sq], None = all) go to the positions after cache_lens, packed.
     ``lens_out`` (int32 [B], not cache_lens) receives the new lengths."""
-    _need(k_new, "k_new", dims=4)
-    _need(v_new, "v_new", k_new.dtype, 4)
+    if k_new.dim() != 4:
+        raise ValueError("k_new must be [B, Sq, Hkv, d]")
     B, Sq, Hkv, d = k_new.shape
-    if v_new.shape != k_new.shape or tuple(k_pages.shape[2:]) != (Hkv, d):
+    _check_cache(B, k_new.dtype, k_pages, v_pages, page_table, cache_lens, k_exp, v_exp)
+    _like(v_new, "v_new", k_new.shape, k_new.dtype)
+    if k_pages.shape[2] != Hkv or k_pages.shape[3] != d:
         raise ValueError("k_new/v_new must be [B, Sq, Hkv, d] with the pools' heads")
     mbs = 0
     if token_mask is not None:
-        _need(token_mask, "token_mask", torch.uint8)
         mbs = _mask_stride(token_mask, B, Sq)
+        _like(token_mask, "token_mask", token_mask.shape, torch.uint8)
     if lens_out is not None:
-        _need(lens_out, "lens_out", torch.int32, 1)
-        if lens_out.shape[0] != B:
-            raise ValueError("lens_out must be [B]")
-    desc = _paged_desc(B, Sq, Hkv, k_new.dtype, k_pages, v_pages, page_table, cache_lens, k_exp,
-                       v_exp, mask_stride=mbs)
-    _one_device(k_new, v_new, k_pages, v_pages, page_table, cache_lens, token_mask, k_exp, v_exp,
-                lens_out)
-    rc = lib().pi_attn_cache_write(
-        ctypes.byref(desc), _ptr(k_new), _ptr(v_new), _ptr(token_mask), _ptr(page_table),
-        _ptr(cache_lens), _ptr(k_pages), _ptr(v_pages), _ptr(k_exp), _ptr(v_exp), _ptr(lens_out),
-        ctypes.c_void_p(_stream(stream)))
+        _like(lens_out, "lens_out", (B,), torch.int32)
+    addresses = _addresses(k_new, v_new, token_mask, page_table, cache_lens, k_pages, v_pages,
+                           k_exp, v_exp, lens_out)
+    desc = _paged_desc(B, Sq, Hkv, k_new.dtype, k_pages, page_table, mask_stride=mbs)[0]
+    rc = lib().pi_attn_cache_write(desc, *addresses, _handle(stream))
     if rc != PI_OK:
         raise PiAttnError(rc, "pi_attn_cache_write")
     return lens_out
@@ -552,26 +596,24 @@ def pi_attn_cache_read(k_pages, v_pages, page_table, cache_lens, S, dtype=torch.
     pi_attn_suffix takes them (``k_cache``, ``v_cache``, ``cache_valid``).
     Returns (k, v, valid), allocated where not given."""
     B, S = cache_lens.shape[0], int(S)
-    desc = _paged_desc(B, S, k_pages.shape[2], dtype, k_pages, v_pages, page_table, cache_lens,
-                       k_exp, v_exp)
+    _check_cache(B, dtype, k_pages, v_pages, page_table, cache_lens, k_exp, v_exp)
     shape = (B, S, *k_pages.shape[2:])
-    with _on(stream):
-        if k_out is None:
-            k_out = torch.empty(shape, dtype=dtype, device=k_pages.device)
-        if v_out is None:
-            v_out = torch.empty(shape, dtype=dtype, device=k_pages.device)
-        if valid_out is None:
-            valid_out = torch.empty((B, S), dtype=torch.uint8, device=k_pages.device)
-    _need(k_out, "k_out", dtype, 4)
-    _need(v_out, "v_out", dtype, 4)
-    _need(valid_out, "valid_out", torch.uint8, 2)
-    if k_out.shape != shape or v_out.shape != shape or valid_out.shape != shape[:2]:
-        raise ValueError("k_out/v_out must be [B, S, Hkv, d] and valid_out [B, S]")
-    _one_device(k_pages, v_pages, page_table, cache_lens, k_exp, v_exp, k_out, v_out, valid_out)
-    rc = lib().pi_attn_cache_read(
-        ctypes.byref(desc), _ptr(k_pages), _ptr(v_pages), _ptr(k_exp), _ptr(v_exp),
-        _ptr(page_table), _ptr(cache_lens), _ptr(k_out), _ptr(v_out), _ptr(valid_out),
-        ctypes.c_void_p(_stream(stream)))
+    if k_out is None:
+        k_out = _empty(shape, dtype, k_pages, stream)
+    else:
+        _like(k_out, "k_out", shape, dtype)
+    if v_out is None:
+        v_out = _empty(shape, dtype, k_out, stream)
+    else:
+        _like(v_out, "v_out", shape, dtype)
+    if valid_out is None:
+        valid_out = _empty(shape[:2], torch.uint8, k_pages, stream)
+    else:
+        _like(valid_out, "valid_out", shape[:2], torch.uint8)
+    addresses = _addresses(k_pages, v_pages, k_exp, v_exp, page_table, cache_lens, k_out, v_out,
+                           valid_out)
+    desc = _paged_desc(B, S, shape[2], dtype, k_pages, page_table)[0]
+    rc = lib().pi_attn_cache_read(desc, *addresses, _handle(stream))
     if rc != PI_OK:
         raise PiAttnError(rc, "pi_attn_cache_read")
     return k_out, v_out, valid_out
@@ -581,9 +623,8 @@ def pi_attn_paged_workspace_bytes(q, k_new, k_pages, v_pages, page_table, cache_
                                   k_exp=None, v_exp=None, window=0, sinks=0):
     """Bytes of workspace pi_attn_paged needs for these tensors (0 if none)."""
     B, Sq, Hq, _ = q.shape
-    desc = _paged_desc(B, Sq, Hq, q.dtype, k_pages, v_pages, page_table, cache_lens, k_exp, v_exp,
-                       window, sinks)
-    return int(lib().pi_attn_paged_workspace_bytes(ctypes.byref(desc)))
+    _check_cache(B, q.dtype, k_pages, v_pages, page_table, cache_lens, k_exp, v_exp)
+    return _paged_desc(B, Sq, Hq, q.dtype, k_pages, page_table, window, sinks)[1]
 
 
 def pi_attn_paged(q, k_new, v_new, k_pages, v_pages, page_table, cache_lens, ar_mask,
@@ -598,45 +639,40 @@ def pi_attn_paged(q, k_new, v_new, k_pages, v_pages, page_table, cache_lens, ar_
     [B,Sq,Hq] receives the log-sum-exp.  ``workspace``: a CUDA uint8 tensor of
     pi_attn_paged_workspace_bytes bytes (allocated here if None and needed).
     Returns ``out`` (allocated if None)."""
-    _need(q, "q", dims=4)
-    _need(k_new, "k_new", q.dtype, 4)
-    _need(v_new, "v_new", q.dtype, 4)
-    _need(ar_mask, "ar_mask", torch.uint8)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Sq, Hq, d]")
     B, Sq, Hq, d = q.shape
+    _check_cache(B, q.dtype, k_pages, v_pages, page_table, cache_lens, k_exp, v_exp)
+    if k_pages.shape[3] != d:
+        raise ValueError("the pools must have q's d")
     shape = (B, Sq, k_pages.shape[2], d)
-    if k_new.shape != shape or v_new.shape != shape or k_pages.shape[3] != d:
-        raise ValueError("k_new/v_new must be [B, Sq, Hkv, d] with the pools' heads and q's d")
+    _like(k_new, "k_new", shape, q.dtype)
+    _like(v_new, "v_new", shape, q.dtype)
     mbs = _mask_stride(ar_mask, B, Sq)
+    _like(ar_mask, "ar_mask", ar_mask.shape, torch.uint8)
     if segment_ids is not None:
-        _need(segment_ids, "segment_ids", torch.int32)
-        if segment_ids.shape != ar_mask.shape:
-            raise ValueError("segment_ids must have the layout of ar_mask")
+        _like(segment_ids, "segment_ids", ar_mask.shape, torch.int32)
     if lse is not None:
-        _need(lse, "lse", torch.float32, 3)
-        if lse.shape != q.shape[:3]:
-            raise ValueError("lse must be [B, Sq, Hq]")
-    desc = _paged_desc(B, Sq, Hq, q.dtype, k_pages, v_pages, page_table, cache_lens, k_exp, v_exp,
-                       window, sinks, softmax_scale, mbs)
-    need = int(lib().pi_attn_paged_workspace_bytes(ctypes.byref(desc)))
-    if out is None or (workspace is None and need > 0):
-        with _on(stream):
-            if out is None:
-                out = torch.empty_like(q)
-            if workspace is None and need > 0:
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _need(out, "out", q.dtype, 4)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
+        _like(lse, "lse", (B, Sq, Hq), torch.float32)
+    if out is not None:
+        _like(out, "out", q.shape, q.dtype)
+    (q_, k_, v_, ar_, seg_, kp_, vp_, ke_, ve_, table_, lens_, out_, lse_, ws_) = _addresses(
+        q, k_new, v_new, ar_mask, segment_ids, k_pages, v_pages, k_exp, v_exp, page_table,
+        cache_lens, out, lse, workspace)
+    desc, need, _ = _paged_desc(B, Sq, Hq, q.dtype, k_pages, page_table, window, sinks,
+                                softmax_scale, mbs)
+    if out is None:
+        out = _empty(q.shape, q.dtype, q, stream)
+        out_ = out.data_ptr()
+    ws_bytes = 0
     if workspace is not None:
-        _need(workspace, "workspace", torch.uint8)
-    _one_device(q, k_new, v_new, k_pages, v_pages, page_table, cache_lens, ar_mask, segment_ids,
-                k_exp, v_exp, out, lse, workspace)
-    ws_bytes = 0 if workspace is None else workspace.numel()
-    rc = lib().pi_attn_paged(
-        ctypes.byref(desc), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(ar_mask), _ptr(segment_ids),
-        _ptr(k_pages), _ptr(v_pages), _ptr(k_exp), _ptr(v_exp), _ptr(page_table),
-        _ptr(cache_lens), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
-        ctypes.c_void_p(_stream(stream)))
+        _like(workspace, "workspace", workspace.shape, torch.uint8)
+        ws_bytes = workspace.numel()
+    elif need > 0:
+        workspace = _empty((need,), torch.uint8, q, stream)
+        ws_, ws_bytes = workspace.data_ptr(), need
+    rc = lib().pi_attn_paged(desc, q_, k_, v_, ar_, seg_, kp_, vp_, ke_, ve_, table_, lens_, out_,
+                             lse_, ws_, ws_bytes, _handle(stream))
     if rc != PI_OK:
         raise PiAttnError(rc, "pi_attn_paged")
     return out
