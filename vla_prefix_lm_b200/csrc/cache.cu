@@ -17,7 +17,7 @@
 // Both kernels move each byte once and are bound by HBM (long calls) or by
 // launch latency (a token per sequence).  d / 8 lanes own one vector, 8
 // elements each (16 bytes of bf16), so a warp access is a contiguous run; the
-// amax is d / 8 lanes of shuffles; a thread keeps the loads of kRows tokens'
+// amax is one warp reduction (d / 8 lanes of shuffles below d = 256); a thread keeps the loads of kRows tokens'
 // keys and values in flight.
 #include <algorithm>
 
@@ -31,16 +31,41 @@ namespace {
 constexpr int kCacheThreads = 128;
 constexpr int kRows = 4;                    // vectors per thread and tensor
 
+// Eight elements as they lie in memory, and as floats.
 struct F8 { float x[8]; };
+template <typename T> struct Raw;
+template <> struct Raw<float> { uint4 a, b; };
+template <> struct Raw<__nv_bfloat16> { uint4 a; };
+template <> struct Raw<E4M3> { uint2 a; };
 
-__device__ __forceinline__ F8 load8(const float* p) {
-  const float4 a = *reinterpret_cast<const float4*>(p);
-  const float4 b = *reinterpret_cast<const float4*>(p + 4);
-  return F8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+__device__ __forceinline__ void zero(Raw<float>& r) { r.a = r.b = make_uint4(0u, 0u, 0u, 0u); }
+__device__ __forceinline__ void zero(Raw<__nv_bfloat16>& r) { r.a = make_uint4(0u, 0u, 0u, 0u); }
+__device__ __forceinline__ void zero(Raw<E4M3>& r) { r.a = make_uint2(0u, 0u); }
+
+__device__ __forceinline__ void load(const float* p, Raw<float>& r) {
+  r.a = *reinterpret_cast<const uint4*>(p);
+  r.b = *reinterpret_cast<const uint4*>(p + 4);
 }
-__device__ __forceinline__ F8 load8(const __nv_bfloat16* p) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void load(const __nv_bfloat16* p, Raw<__nv_bfloat16>& r) {
+  r.a = *reinterpret_cast<const uint4*>(p);
+}
+__device__ __forceinline__ void load(const E4M3* p, Raw<E4M3>& r) {
+  r.a = *reinterpret_cast<const uint2*>(p);
+}
+__device__ __forceinline__ void store(float* p, const Raw<float>& r) {
+  *reinterpret_cast<uint4*>(p) = r.a;
+  *reinterpret_cast<uint4*>(p + 4) = r.b;
+}
+__device__ __forceinline__ void store(__nv_bfloat16* p, const Raw<__nv_bfloat16>& r) {
+  *reinterpret_cast<uint4*>(p) = r.a;
+}
+__device__ __forceinline__ F8 floats(const Raw<float>& r) {
+  return F8{{__uint_as_float(r.a.x), __uint_as_float(r.a.y), __uint_as_float(r.a.z),
+             __uint_as_float(r.a.w), __uint_as_float(r.b.x), __uint_as_float(r.b.y),
+             __uint_as_float(r.b.z), __uint_as_float(r.b.w)}};
+}
+__device__ __forceinline__ F8 floats(const Raw<__nv_bfloat16>& r) {
+  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
   F8 f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -49,12 +74,11 @@ __device__ __forceinline__ F8 load8(const __nv_bfloat16* p) {
   }
   return f;
 }
-__device__ __forceinline__ F8 load8(const E4M3* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
+__device__ __forceinline__ F8 floats(const Raw<E4M3>& r) {
   F8 f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t w = i < 2 ? u.x : u.y;
+    const uint32_t w = i < 2 ? r.a.x : r.a.y;
     const float2 v = e4m3x2_to_float2((uint16_t)(w >> (16 * (i & 1))));
     f.x[2 * i] = v.x;
     f.x[2 * i + 1] = v.y;
@@ -82,27 +106,71 @@ __device__ __forceinline__ void store8(E4M3* p, const F8& f) {
 template <typename T> constexpr bool kIsE4M3 = false;
 template <> constexpr bool kIsE4M3<E4M3> = true;
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
-// The exponent byte of a vector with largest magnitude amax (NaN if it holds
-// one): 448 = 1.75 * 2^8, so amax = 1.M * 2^(E - 127) needs e = E - 135, one more
-// if 1.M > 1.75.  Zero vectors take scale 1.
-__device__ __forceinline__ uint32_t exp_byte(float amax) {
-  const uint32_t u = __float_as_uint(amax);
+// The exponent byte of a vector whose largest magnitude has the bits u (above
+// infinity's: a NaN): 448 = 1.75 * 2^8, so 1.M * 2^(E - 127) needs e = E - 135, one
+// more if 1.M > 1.75.  Zero vectors take scale 1.
+__device__ __forceinline__ uint32_t exp_byte(uint32_t u) {
   if (u == 0) return 127u;
   if (u > 0x7F800000u) return 255u;
   const int byte = (int)(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   return (uint32_t)max(byte, 1);
 }
 
-// One CTA takes `tok` consecutive new tokens of one sequence.  A token's
-// position is the sequence's cached length plus the valid tokens before it:
-// the CTA counts the mask bytes before its run, and one ballot per 32 tokens
-// ranks its own.
+// The largest magnitude of eight elements, as the bits of a float: magnitudes
+// compare as integers, and a NaN's is the largest.  bf16: two at a time.
+__device__ __forceinline__ uint32_t magnitude(const Raw<float>& r) {
+  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+  return m;
+}
+__device__ __forceinline__ uint32_t magnitude(const Raw<__nv_bfloat16>& r) {
+  const uint32_t k = 0x7FFF7FFFu;
+  const uint32_t m = __vmaxu2(__vmaxu2(r.a.x & k, r.a.y & k), __vmaxu2(r.a.z & k, r.a.w & k));
+  return max(m & 0xFFFF0000u, m << 16);
+}
+// The elements times 2^(biased - 127), exact (what would fall under the type's
+// range is far under e4m3's).
+__device__ __forceinline__ F8 scaled(const Raw<float>& r, uint32_t biased) {
+  F8 f = floats(r);
+  const float s = __uint_as_float(biased << 23);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f.x[e] *= s;
+  return f;
+}
+__device__ __forceinline__ F8 scaled(const Raw<__nv_bfloat16>& r, uint32_t biased) {
+  const uint32_t s = (biased << 7) * 0x10001u;
+  Raw<__nv_bfloat16> x;
+  x.a = make_uint4(mul_bf16x2(r.a.x, s), mul_bf16x2(r.a.y, s), mul_bf16x2(r.a.z, s),
+                   mul_bf16x2(r.a.w, s));
+  return floats(x);
+}
+
+// Valid tokens among mask[0 .. n): the thread's share, 16 bytes at a time where
+// the row is aligned.
+__device__ __forceinline__ int count_valid(const uint8_t* mask, int n) {
+  int cnt = 0, t = 0;
+  if ((reinterpret_cast<uintptr_t>(mask) & 15u) == 0) {
+    t = n & ~15;
+    for (int i = threadIdx.x * 16; i < t; i += kCacheThreads * 16) {
+      const uint4 v = *reinterpret_cast<const uint4*>(mask + i);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        cnt += __popc((w[k] | ((w[k] & 0x7F7F7F7Fu) + 0x7F7F7F7Fu)) & 0x80808080u);
+    }
+  }
+  for (t += threadIdx.x; t < n; t += kCacheThreads) cnt += mask[t] != 0 ? 1 : 0;
+  return cnt;
+}
+
+// One CTA takes `tok` consecutive new tokens of one sequence, one pass of its
+// threads.  The vectors are loaded first: where they go takes three dependent
+// lookups (length and mask, page, slot), which the loads cover.  A token's
+// position is the sequence's cached length plus the valid tokens before it: the
+// CTA counts the mask bytes before its run, and one ballot per 32 tokens ranks
+// its own.
 template <typename TIn, typename TC>
 __global__ void __launch_bounds__(kCacheThreads)
     cache_write_kernel(const __grid_constant__ CacheParams p, const DevCtl ctl, int tok) {
@@ -113,15 +181,36 @@ __global__ void __launch_bounds__(kCacheThreads)
   const int b = blockIdx.y, t0 = blockIdx.x * tok;
   const int nt = min(tok, p.S - t0);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lpv = p.d >> 3;                  // lanes per vector
+  const int n_vec = nt * p.Hkv;              // vectors of each tensor in the run
+  const int vpb = kCacheThreads / lpv;       // vectors per row of the pass
+  const int vi = threadIdx.x / lpv, e0 = (threadIdx.x % lpv) * 8;
+  const long long src0 = ((long long)b * p.S + t0) * p.Hkv;
+  const TIn* kin = static_cast<const TIn*>(p.k_in);
+  const TIn* vin = static_cast<const TIn*>(p.v_in);
+  Raw<TIn> kr[kRows], vr[kRows];
+  auto fetch = [&](int v0) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int v = v0 + i * vpb + vi;
+      if (v < n_vec) {
+        load(kin + (src0 + v) * p.d + e0, kr[i]);
+        load(vin + (src0 + v) * p.d + e0, vr[i]);
+      } else {
+        zero(kr[i]);
+        zero(vr[i]);
+      }
+    }
+  };
+  fetch(0);
+
   const uint8_t* tm = p.tmask ? p.tmask + (long long)b * p.tmask_bs : nullptr;
   const long long cap = (long long)p.max_pages << p.page_shift;
   bool bad = false;
   const int len = cached_len(p.lens, b, p.max_pages, p.page_shift, bad);
-
   int before = t0;                           // valid tokens before the run
   if (tm) {
-    int cnt = 0;
-    for (int t = threadIdx.x; t < t0; t += kCacheThreads) cnt += tm[t] != 0 ? 1 : 0;
+    int cnt = count_valid(tm, t0);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) cnt += __shfl_xor_sync(0xffffffffu, cnt, off);
     if (lane == 0) s_count[warp] = cnt;
@@ -160,66 +249,42 @@ __global__ void __launch_bounds__(kCacheThreads)
   }
   __syncthreads();
 
-  const int lpv = p.d >> 3;                  // lanes per vector
-  const int n_vec = nt * p.Hkv;              // vectors of each tensor in the run
-  const int vpb = kCacheThreads / lpv;       // vectors per pass of the CTA
-  const int vi = threadIdx.x / lpv, e0 = (threadIdx.x % lpv) * 8;
-  const long long src0 = ((long long)b * p.S + t0) * p.Hkv;
-  const TIn* kin = static_cast<const TIn*>(p.k_in);
-  const TIn* vin = static_cast<const TIn*>(p.v_in);
   TC* kp = static_cast<TC*>(p.kp);
   TC* vp = static_cast<TC*>(p.vp);
   for (int v0 = 0; v0 < n_vec; v0 += vpb * kRows) {
-    F8 kx[kRows], vx[kRows];
-    long long dst[kRows];
+    if (v0 > 0) fetch(v0);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const int v = v0 + i * vpb + vi;
-      dst[i] = -1;
-      if (v < n_vec) {
-        const int slot = s_slot[v / p.Hkv];
-        if (slot >= 0) {
-          dst[i] = (long long)slot * p.Hkv + v % p.Hkv;
-          kx[i] = load8(kin + (src0 + v) * p.d + e0);
-          vx[i] = load8(vin + (src0 + v) * p.d + e0);
-        }
-      }
-      if (dst[i] < 0) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) kx[i].x[e] = vx[i].x[e] = 0.f;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+      const int t = p.Hkv == 1 ? v : v / p.Hkv;
+      const int slot = v < n_vec ? s_slot[t] : -1;
+      const long long dst = (long long)(slot - t) * p.Hkv + v;   // slot * Hkv + v % Hkv
       if constexpr (kIsE4M3<TC>) {
-        float ka = 0.f, va = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          ka = max_nan(ka, fabsf(kx[i].x[e]));
-          va = max_nan(va, fabsf(vx[i].x[e]));
-        }
-        for (int off = lpv >> 1; off > 0; off >>= 1) {
-          ka = max_nan(ka, __shfl_xor_sync(0xffffffffu, ka, off));
-          va = max_nan(va, __shfl_xor_sync(0xffffffffu, va, off));
+        uint32_t ka = magnitude(kr[i]), va = magnitude(vr[i]);
+        if (lpv == 32) {
+          ka = __reduce_max_sync(0xffffffffu, ka);
+          va = __reduce_max_sync(0xffffffffu, va);
+        } else {
+          for (int off = lpv >> 1; off > 0; off >>= 1) {
+            ka = max(ka, __shfl_xor_sync(0xffffffffu, ka, off));
+            va = max(va, __shfl_xor_sync(0xffffffffu, va, off));
+          }
         }
         const uint32_t kb = exp_byte(ka), vb = exp_byte(va);
         // 2^-e = 2^(127 - byte): biased exponent 254 - byte, in [7, 253] (a NaN
         // vector: 0, what it holds does not matter)
-        const float ks = __uint_as_float((254u - min(kb, 254u)) << 23);
-        const float vs = __uint_as_float((254u - min(vb, 254u)) << 23);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          kx[i].x[e] *= ks;
-          vx[i].x[e] *= vs;
+        const F8 kx = scaled(kr[i], 254u - min(kb, 254u)), vx = scaled(vr[i], 254u - min(vb, 254u));
+        if (slot >= 0) {
+          store8(kp + dst * p.d + e0, kx);
+          store8(vp + dst * p.d + e0, vx);
+          if (e0 == 0) {
+            p.ke[dst] = (uint8_t)kb;
+            p.ve[dst] = (uint8_t)vb;
+          }
         }
-        if (dst[i] >= 0 && e0 == 0) {
-          p.ke[dst[i]] = (uint8_t)kb;
-          p.ve[dst[i]] = (uint8_t)vb;
-        }
-      }
-      if (dst[i] >= 0) {
-        store8(kp + dst[i] * p.d + e0, kx[i]);
-        store8(vp + dst[i] * p.d + e0, vx[i]);
+      } else if (slot >= 0) {
+        store(kp + dst * p.d + e0, kr[i]);
+        store(vp + dst * p.d + e0, vr[i]);
       }
     }
   }
@@ -263,39 +328,45 @@ __global__ void __launch_bounds__(kCacheThreads)
   TOut* ko = static_cast<TOut*>(p.k_out);
   TOut* vo = static_cast<TOut*>(p.v_out);
   for (int v0 = 0; v0 < n_vec; v0 += vpb * kRows) {
-    F8 kx[kRows], vx[kRows];
-    float ks[kRows], vs[kRows];
+    Raw<TC> kr[kRows], vr[kRows];
+    uint8_t kb[kRows], vb[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const int v = v0 + i * vpb + vi;
-      const int slot = v < n_vec ? s_slot[v / p.Hkv] : -1;
-      ks[i] = vs[i] = 1.f;
+      const int t = p.Hkv == 1 ? v : v / p.Hkv;
+      const int slot = v < n_vec ? s_slot[t] : -1;
+      kb[i] = vb[i] = 127;
+      zero(kr[i]);
+      zero(vr[i]);
       if (slot >= 0) {
-        const long long src = (long long)slot * p.Hkv + v % p.Hkv;
-        kx[i] = load8(kp + src * p.d + e0);
-        vx[i] = load8(vp + src * p.d + e0);
+        const long long src = (long long)(slot - t) * p.Hkv + v;   // slot * Hkv + v % Hkv
+        load(kp + src * p.d + e0, kr[i]);
+        load(vp + src * p.d + e0, vr[i]);
         if constexpr (kIsE4M3<TC>) {
-          ks[i] = exp_scale(p.ke[src]);
-          vs[i] = exp_scale(p.ve[src]);
+          kb[i] = p.ke[src];
+          vb[i] = p.ve[src];
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) kx[i].x[e] = vx[i].x[e] = 0.f;
       }
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const int v = v0 + i * vpb + vi;
       if (v >= n_vec) continue;
+      const long long at = (dst0 + v) * p.d + e0;
       if constexpr (kIsE4M3<TC>) {
+        F8 kx = floats(kr[i]), vx = floats(vr[i]);
+        const float ks = exp_scale(kb[i]), vs = exp_scale(vb[i]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          kx[i].x[e] *= ks[i];
-          vx[i].x[e] *= vs[i];
+          kx.x[e] *= ks;
+          vx.x[e] *= vs;
         }
+        store8(ko + at, kx);
+        store8(vo + at, vx);
+      } else {
+        store(ko + at, kr[i]);
+        store(vo + at, vr[i]);
       }
-      store8(ko + (dst0 + v) * p.d + e0, kx[i]);
-      store8(vo + (dst0 + v) * p.d + e0, vx[i]);
     }
   }
 }
@@ -310,6 +381,7 @@ int tokens_per_cta(const CacheParams& p) {
   return tok;
 }
 
+// (Pools and dense tensors share a type unless the pool is e4m3.)
 template <typename T, typename TC>
 cudaError_t launch(const CacheParams& p, bool write, const DevCtl& ctl, cudaStream_t st) {
   const int tok = tokens_per_cta(p);
