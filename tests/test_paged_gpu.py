@@ -155,7 +155,8 @@ def test_decode_heads(Hq, Hkv, cache):
 
 @pytest.mark.parametrize("cache", CACHES)
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
-@pytest.mark.parametrize("lens,Sq", [([0], 2), ([33, 700], 3), ([816, 0, 130], 51), ([5], 300)])
+@pytest.mark.parametrize("lens,Sq", [([0], 2), ([33, 700], 3), ([816, 0, 130], 51), ([5], 300),
+                                     ([200, 3], 700)])
 def test_chunk(lens, Sq, page, cache):
     _attend(3, lens, Sq, cache, page, mask="suffix")
 
@@ -175,7 +176,7 @@ def test_window_and_sinks(Sq, window, sinks, cache):
 
 
 @pytest.mark.parametrize("cache", CACHES)
-@pytest.mark.parametrize("Sq,window", [(1, 0), (7, 0), (7, 40), (150, 0), (150, 90), (300, 3)])
+@pytest.mark.parametrize("Sq,window", [(1, 0), (7, 0), (7, 40), (150, 0), (150, 90), (300, 3), (600, 200)])
 def test_segments_and_padding(Sq, window, cache):
     _attend(6, [130, 0, 45, 260], Sq, cache, 16, mask="segments", pad=True, batch_mask=True,
             window=window, sinks=2, Hkv=2)

@@ -159,6 +159,14 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
   return n >= 32 ? ~0u : (n <= 0 ? 0u : (1u << n) - 1u);
 }
 
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
                "r"(v.w)
@@ -174,9 +182,10 @@ __device__ __forceinline__ bool in_window(int len, int i, int j, int window, int
 // (paged_tc.cu).  Sequences are scheduled in groups of kPagedTcGroup.
 constexpr int kPagedTcGroup = 64;
 struct PagedTcParams : PagedParams {
-  CUtensorMap map_k, map_v;  // bf16 pools, if use_tma
+  CUtensorMap map_k, map_v;  // the pools, if use_tma (there is a page)
   int use_tma;
   float* ws;                 // partials [n_clusters * 2][256 rows][256], then (m, l)
+  uint16_t* codes;           // chunks over 512 tokens: the CTAs' codes
   int G, g_shift;            // heads per kv head (a power of two), its logarithm
   int tok_per_tile;          // new tokens per 256-row tile
   int n_tiles;               // query tiles per (sequence, kv head)

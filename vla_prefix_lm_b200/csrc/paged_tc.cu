@@ -19,8 +19,8 @@
 //     window or of padding tokens, so that whatever a stale slot holds (NaN)
 //     meets P = 0 as 0.  (Gathering every tile this way held a CTA to 11 bytes
 //     a cycle, about 5700 cycles a tile.)
-//   e4m3: 16-byte loads held in registers one tile ahead (32 KB raw per CTA in
-//     flight), then rebuilt as bf16 exactly, as the scale is a power of two: no
+//   e4m3: raw rows by TMA into a staging half ahead of their use, then rebuilt as
+//     bf16 by the loader warps, exactly, as the scale is a power of two: no
 //     rounding beside the cache's own.
 //
 // Work.  Unit = (sequence, kv head, query tile).  Lengths differ by sequence
@@ -44,8 +44,9 @@
 //   warp 14      scheduler: derives the segments this cluster runs and hands
 //                them to the other warps through a two-entry ring
 // TMEM per CTA (512 columns): O fp32 [0,256) | S0 [256,384) | S1 [384,512).
-// Shared memory per CTA: Q 64 KB | K ring 2 x 32 KB | V ring 2 or 4 x 16 KB |
-// P 32 KB (also the output staging area) | control | chunk token codes.
+// Shared memory per CTA: Q 64 KB | K ring 2 x 32 KB | V ring 4 x 16 KB, or 2 and
+// 32 KB of raw e4m3 rows | P 32 KB (also the output staging area) | control | codes
+// of up to 512 chunk tokens (longer chunks: in the workspace).
 // Every wait is bounded (DevCtl); counters that index barriers and ring slots
 // run across segments.
 #include <cfloat>
@@ -97,15 +98,20 @@ struct Segment {
   int any_e;                 // an expert among the tokens
 };
 
-template <int kNV_, int kMaxTok_>
+// bf16 pages: four V halves.  e4m3: two, and as much room for raw rows, half an
+// item each: K 2 x [32 keys x 256 bytes], V 2 x [64 keys x 128 bytes].
+constexpr int kRawHalf = 8192;
+template <bool kE4M3>
 struct Layout {
-  static constexpr int kNV = kNV_;
-  static constexpr int kMaxTok = kMaxTok_;
-  static constexpr int kTiles = (kMaxTok + kBN - 1) / kBN;
+  static constexpr int kNV = kE4M3 ? 2 : 4;
   static constexpr int kOffV = kOffK + kNK * kKItem;
-  static constexpr int kOffP = kOffV + kNV * kVItem;
+  static constexpr int kOffRaw = kOffV + kNV * kVItem;
+  static constexpr int kOffP = kOffRaw + (kE4M3 ? 4 * kRawHalf : 0);
   static constexpr int kOffCtl = kOffP + kPBytes;
 };
+constexpr int kTiles = (kMaxTokens + kBN - 1) / kBN;
+// Codes of longer chunks live in the workspace (one copy per CTA).
+constexpr int kSmemTokens = 512;
 
 // The schedule's inputs: nominal tiles before each sequence's units, lengths.
 struct Plan {
@@ -124,13 +130,14 @@ struct __align__(8) Smem {
   uint64_t drain_qk, drain_pv;
   uint64_t pair[4];                 // a quarter's two warps meet
   uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t raw_full[4], raw_empty[4];   // e4m3: K halves, V halves (this CTA's)
   uint32_t tmem_base;
   int abort;
   Plan plan;
   Segment seg[kSegs];
-  uint16_t tile_cs_first[L::kTiles];
-  uint16_t tile_cs_last[L::kTiles];
-  uint8_t tile_fast[L::kTiles];
+  uint16_t tile_cs_first[kTiles];
+  uint16_t tile_cs_last[kTiles];
+  uint8_t tile_fast[kTiles];
 };
 
 template <class L>
@@ -139,13 +146,11 @@ __host__ __device__ constexpr int off_codes() {
 }
 __host__ __device__ constexpr int pad_tokens(int n) { return (n + 127) / 128 * 128; }
 template <class L>
-__host__ __device__ constexpr int layout_bytes(int n_tok) {
-  return off_codes<L>() + pad_tokens(n_tok) * 2;
+__host__ __device__ constexpr int layout_bytes() {
+  return off_codes<L>() + kSmemTokens * 2;
 }
-using LayoutLong = Layout<2, kMaxTokens>;
-using LayoutShort = Layout<4, 512>;         // four V halves beside a short chunk's codes
-static_assert(layout_bytes<LayoutLong>(kMaxTokens) <= kSmemLimit, "layout too large");
-static_assert(layout_bytes<LayoutShort>(512) <= kSmemLimit, "short layout too large");
+static_assert(layout_bytes<Layout<false>>() <= kSmemLimit, "layout too large");
+static_assert(layout_bytes<Layout<true>>() <= kSmemLimit, "layout too large");
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -455,6 +460,17 @@ __device__ __forceinline__ int page_of(const PagedTcParams& p, const Segment& s,
   if (x >= s.len || (p.window > 0 && x < s.lo0 && x >= p.sinks)) return kNoRow;
   return p.table[(long long)s.b * p.max_pages + (x >> p.page_shift)];
 }
+// Whether some query of the segment sees cached position x.
+__device__ __forceinline__ bool row_seen(const PagedTcParams& p, const Segment& s, int x) {
+  return x < s.len && (p.window <= 0 || x >= s.lo0 || x < p.sinks);
+}
+// The page id at x if some query sees a row of that page inside x's tile (the
+// table may hold anything for others).
+__device__ __forceinline__ int page_seen(const PagedTcParams& p, const Segment& s, int x) {
+  const int w = min(1 << p.page_shift, kBN), x0 = x & -w;
+  if (x0 >= s.len || (p.window > 0 && x0 + w <= s.lo0 && x0 >= p.sinks)) return kNoRow;
+  return p.table[(long long)s.b * p.max_pages + (x0 >> p.page_shift)];
+}
 // Its slot; -1 if there is none (a page id out of range is noted in bad).
 __device__ __forceinline__ int slot_of(const PagedTcParams& p, int x, int page, bool& bad) {
   if (page >= 0 && page < p.num_pages)
@@ -492,96 +508,30 @@ __device__ __noinline__ void copy_rows(int mine, const uint8_t* base, uint32_t p
   }
 }
 
-// 16 raw bytes of each of two rows -> two 16-byte chunks of bf16 each, at shared
-// addresses a0, a1 and b0, b1; m: their scales (main_scale).  Not inlined: the
-// loaders' unrolled conversions (16 KB of code a warp) beside the softmax's
-// starved every warp of instructions.
-template <bool kRest>
-__device__ __noinline__ void put_pair(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1, uint4 wa,
-                                      uint4 wb, uint32_t ma, uint32_t mb, uint32_t ra, uint32_t rb) {
-  uint2 qa[4] = {dequant4(wa.x, ma), dequant4(wa.y, ma), dequant4(wa.z, ma), dequant4(wa.w, ma)};
-  uint2 qb[4] = {dequant4(wb.x, mb), dequant4(wb.y, mb), dequant4(wb.z, mb), dequant4(wb.w, mb)};
-  if (kRest) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      qa[i] = make_uint2(mul_bf16x2(qa[i].x, ra), mul_bf16x2(qa[i].y, ra));
-      qb[i] = make_uint2(mul_bf16x2(qb[i].x, rb), mul_bf16x2(qb[i].y, rb));
-    }
-  }
-  st_shared_v4(a0, make_uint4(qa[0].x, qa[0].y, qa[1].x, qa[1].y));
-  st_shared_v4(a1, make_uint4(qa[2].x, qa[2].y, qa[3].x, qa[3].y));
-  st_shared_v4(b0, make_uint4(qb[0].x, qb[0].y, qb[1].x, qb[1].y));
-  st_shared_v4(b1, make_uint4(qb[2].x, qb[2].y, qb[3].x, qb[3].y));
-}
-// The N pieces that fetch_rows brought -> an item.  Lane: 16 bytes c16 of row
-// row0 + it * step; scale and exponent of row it sit in lane lane0 + it * lstep.
-template <int N>
-__device__ __forceinline__ void put_rows(uint32_t item, int row0, int step, int c16, int lane0,
-                                         int lstep, const uint4 (&raw)[N], uint32_t e) {
-  const uint32_t m = main_scale(e);
-  const uint32_t base = item + row0 * 128 + (c16 >> 2) * kKBlk;
-  const int c = (c16 & 3) * 2, x0 = row0 & 7, x1 = (row0 + step) & 7;
-  const uint32_t a0 = base + ((c ^ x0) << 4), a1 = base + (((c + 1) ^ x0) << 4);
-  const uint32_t b0 = base + step * 128 + ((c ^ x1) << 4),
-                 b1 = base + step * 128 + (((c + 1) ^ x1) << 4);
-  const bool rest = __any_sync(0xffffffffu, e > 134u && e != kNoExp);     // values above 448 * 2^7
-  const uint32_t r = rest ? rest_scale(e) : 0u;
-#pragma unroll
-  for (int it = 0; it < N; it += 2) {
-    const uint32_t d = it * step * 128;      // (2 * step is a multiple of 8 rows)
-    const uint32_t ma = __shfl_sync(0xffffffffu, m, lane0 + it * lstep);
-    const uint32_t mb = __shfl_sync(0xffffffffu, m, lane0 + (it + 1) * lstep);
-    if (!rest) {
-      put_pair<false>(a0 + d, a1 + d, b0 + d, b1 + d, raw[it], raw[it + 1], ma, mb, 0u, 0u);
-    } else {
-      const uint32_t ra = __shfl_sync(0xffffffffu, r, lane0 + it * lstep);
-      const uint32_t rb = __shfl_sync(0xffffffffu, r, lane0 + (it + 1) * lstep);
-      put_pair<true>(a0 + d, a1 + d, b0 + d, b1 + d, raw[it], raw[it + 1], ma, mb, ra, rb);
-    }
-  }
-}
-
-// N raw pieces of 16 bytes at byte `col` of the rows row_at(0 .. N - 1) of an
-// e4m3 pool.  Rows below 0 read row 0: their scale is 0, and every byte
-// dequantises to a finite number.
-template <int N, class RowAt>
-__device__ __forceinline__ void fetch_rows(const PagedTcParams& p, const void* pool, int col,
-                                           int g, uint4 (&raw)[N], RowAt row_at) {
-  if (p.num_pages == 0) {                    // no row 0 either
-#pragma unroll
-    for (int it = 0; it < N; ++it) raw[it] = make_uint4(0u, 0u, 0u, 0u);
-    return;
-  }
-  const uint8_t* base = static_cast<const uint8_t*>(pool) + g * kD + col;
-  const uint32_t pitch = (uint32_t)p.Hkv * kD;
-  int r[N];
-#pragma unroll
-  for (int it = 0; it < N; ++it) r[it] = max(row_at(it), 0);
-#pragma unroll
-  for (int it = 0; it < N; ++it)
-    raw[it] = __ldg(reinterpret_cast<const uint4*>(base + (unsigned long long)(uint32_t)r[it] * pitch));
-}
 // The exponent byte of row r, loaded by the lane that looked the row up.
 __device__ __forceinline__ uint32_t row_exp(const PagedTcParams& p, const uint8_t* exps, int r, int g) {
   return r >= 0 ? (uint32_t)__ldg(exps + (unsigned long long)(uint32_t)r * (uint32_t)p.Hkv + g) : kNoExp;
 }
 
-template <bool kE4M3, class L>
+template <bool kE4M3>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     paged_tc_kernel(const __grid_constant__ PagedTcParams p, const DevCtl ctl) {
+  using L = Layout<kE4M3>;
   using SmemT = Smem<L>;
   constexpr int kNV = L::kNV;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   // Both CTAs see the same base offset, so both leave here or neither does.
-  if ((int)(smem - smem_raw) + layout_bytes<L>(p.Sq) > p.smem_bytes || p.Sq > L::kMaxTok) {
+  if ((int)(smem - smem_raw) + layout_bytes<L>() > p.smem_bytes) {
     pdl_wait();
     if (threadIdx.x == 0) record_status(ctl, kStatusUnsupported);
     return;
   }
   SmemT& sm = *reinterpret_cast<SmemT*>(smem + L::kOffCtl);
-  uint16_t* codes = reinterpret_cast<uint16_t*>(smem + off_codes<L>());
+  uint16_t* codes = p.Sq <= kSmemTokens
+                        ? reinterpret_cast<uint16_t*>(smem + off_codes<L>())
+                        : p.codes + (long long)blockIdx.x * pad_tokens(p.Sq);
   uint8_t* sQ = smem + kOffQ;
   uint8_t* kring = smem + kOffK;
   uint8_t* vring = smem + L::kOffV;
@@ -616,6 +566,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kSegs; ++s) {
       mbar_init(&sm.seg_full[s], 1);
       mbar_init(&sm.seg_empty[s], kSegUsers);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&sm.raw_full[s], 1);
+      mbar_init(&sm.raw_empty[s], 2);
     }
     sm.abort = 0;
     fence_barrier_init();
@@ -831,12 +785,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int row32 = lane * 2 + lw;                               // 32 lanes per row
     const int row16 = (lane >> 1) * 4 + lw * 2 + (lane & 1);       // 16
     const int row8 = (lane >> 2) * 8 + lw * 4 + (lane & 3);        // 8
-    // e4m3: which of a pass's rows, and which 16-byte piece, this lane has.  Each
-    // eight lanes hold four pieces of two adjacent rows, whose bf16 chunks fall
-    // on eight different bank groups.
-    const int odd = (lane >> 2) & 1;
-    const int sub16 = odd, piece16 = (lane & 3) + 4 * (lane >> 3);
-    const int sub8 = odd + 2 * (lane >> 4), piece8 = (lane & 3) + 4 * ((lane >> 3) & 1);
     // TMA tiles: lane l has the page of box l.
     const int box = min(1 << p.page_shift, 64);                    // rows per box
     const int boxes = 64 / box;                                    // per 64 keys
@@ -844,9 +792,91 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (idx >= px->it0 + px->n) return kNoRow;
       const KeyTile kt = key_tile(*px, idx);
       if (kt.chunk) return kNoRow;
-      const bool tma = !kE4M3 && p.use_tma && whole_tile(p, *px, kt);
-      return page_of(p, *px, kt.tile * kBN + (tma ? tma_row : row));
+      const int at = kt.tile * kBN;
+      if (kE4M3) return page_seen(p, *px, at + row);
+      const bool tma = p.use_tma && whole_tile(p, *px, kt);
+      return page_of(p, *px, at + (tma ? tma_row : row));
     };
+    // e4m3.  Raw halves come by TMA, a tile ahead of their use, all rows of every
+    // page that holds a row some query sees; rows that nobody sees get scale 0
+    // (every byte dequantises to a finite number).  r: raw half (K 0, 1; V 2, 3).
+    uint8_t* const raw = smem + L::kOffRaw;
+    uint32_t raw_n[2] = {0u, 0u};             // fills of this operand's halves
+    auto fetch_raw = [&](const CUtensorMap* map, int r, int rows, int slot_lane, int x, int slot) {
+      if (lw != 0 || !p.use_tma) return;      // slot: of the row this lane looked up
+      const int b = min(1 << p.page_shift, rows), n = rows / b;
+      const int first = __shfl_sync(0xffffffffu, slot, slot_lane + min(lane, n - 1) * (b >> 1));
+      const uint32_t fills = raw_n[r & 1];
+      if (fills > 0) (void)warp_wait(&sm.raw_empty[r], (fills - 1) & 1, sm, ctl);
+      if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[r], kRawHalf);
+      __syncwarp();
+      if (lane < n)
+        tma_load_3d_at(smem_u32(raw + r * kRawHalf + lane * b * (kRawHalf / rows)), map,
+                       &sm.raw_full[r], x, first < 0 ? p.num_pages << p.page_shift : first, px->g);
+    };
+    // A raw half -> bf16 rows of an item.  16 lanes (K) or 8 (V) per row; each
+    // eight lanes hold four 16-byte pieces (c16 ..) of two adjacent rows, whose
+    // bf16 chunks fall on eight different bank groups.  Lane: pieces of rows row0 +
+    // it * step, it < 8, exponent of row it in lane lane0 + it * lstep.
+    auto convert = [&](int r, int row_bytes, uint32_t item, int row0, int step, int c16, int lane0,
+                       int lstep, uint32_t e) -> bool {
+      const uint32_t fills = raw_n[r & 1];
+      if (p.use_tma && !warp_wait(&sm.raw_full[r], fills & 1, sm, ctl)) return false;
+      uint32_t src = smem_u32(raw + r * kRawHalf) + row0 * row_bytes + c16 * 16;
+      const uint32_t base = item + row0 * 128 + (c16 >> 2) * kKBlk;
+      const int c = (c16 & 3) * 2, x0 = row0 & 7, x1 = (row0 + step) & 7;
+      uint32_t a0 = base + ((c ^ x0) << 4), a1 = base + (((c + 1) ^ x0) << 4);
+      uint32_t b0 = base + step * 128 + ((c ^ x1) << 4);
+      uint32_t b1 = base + step * 128 + (((c + 1) ^ x1) << 4);
+      const uint32_t m = main_scale(e);
+      const bool rest = __any_sync(0xffffffffu, e > 134u && e < 255u);   // over 448 * 2^7
+      const uint32_t m2 = rest ? rest_scale(e) : 0u;
+      uint4 wa = ld_shared_v4(src), wb = ld_shared_v4(src + step * row_bytes);
+#pragma unroll 1
+      for (int it = 0; it < 8; it += 2) {
+        const uint32_t ma = __shfl_sync(0xffffffffu, m, lane0 + it * lstep);
+        const uint32_t mb = __shfl_sync(0xffffffffu, m, lane0 + (it + 1) * lstep);
+        uint2 qa[4] = {dequant4(wa.x, ma), dequant4(wa.y, ma), dequant4(wa.z, ma), dequant4(wa.w, ma)};
+        uint2 qb[4] = {dequant4(wb.x, mb), dequant4(wb.y, mb), dequant4(wb.z, mb), dequant4(wb.w, mb)};
+        src += 2 * step * row_bytes;
+        if (it < 6) {
+          wa = ld_shared_v4(src);
+          wb = ld_shared_v4(src + step * row_bytes);
+        }
+        if (rest) {
+          const uint32_t ra = __shfl_sync(0xffffffffu, m2, lane0 + it * lstep);
+          const uint32_t rb = __shfl_sync(0xffffffffu, m2, lane0 + (it + 1) * lstep);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            qa[i] = make_uint2(mul_bf16x2(qa[i].x, ra), mul_bf16x2(qa[i].y, ra));
+            qb[i] = make_uint2(mul_bf16x2(qb[i].x, rb), mul_bf16x2(qb[i].y, rb));
+          }
+        }
+        st_shared_v4(a0, make_uint4(qa[0].x, qa[0].y, qa[1].x, qa[1].y));
+        st_shared_v4(a1, make_uint4(qa[2].x, qa[2].y, qa[3].x, qa[3].y));
+        st_shared_v4(b0, make_uint4(qb[0].x, qb[0].y, qb[1].x, qb[1].y));
+        st_shared_v4(b1, make_uint4(qb[2].x, qb[2].y, qb[3].x, qb[3].y));
+        const uint32_t d = 2 * step * 128;    // (2 * step is a multiple of 8 rows)
+        a0 += d;
+        a1 += d;
+        b0 += d;
+        b1 += d;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.raw_empty[r]);   // the half has been read
+      ++raw_n[r & 1];
+      return true;
+    };
+    // After the last use: a bounded wait for raw halves still on their way.
+    auto land_raw = [&](int r0, const uint32_t (&asked)[2]) {
+      if (kE4M3 && p.use_tma && lw == 0 && lane == 0)
+        for (int h = 0; h < 2; ++h)
+          if (asked[h] > 0) (void)mbar_wait(&sm.raw_full[r0 + h], (asked[h] - 1) & 1, ctl);
+      __syncwarp();
+    };
+    const int odd = (lane >> 2) & 1;
+    const int sub16 = odd, piece16 = (lane & 3) + 4 * (lane >> 3);
+    const int sub8 = odd + 2 * (lane >> 4), piece8 = (lane & 3) + 4 * ((lane >> 3) & 1);
     // The boxes of one item: `blocks` 64-column blocks from block c0 of the
     // head, keys from position x0; lane l brings box l / blocks, block l % blocks
     // (pages of 64 tokens and more: one box of all blocks).  A page id out of
@@ -884,27 +914,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             static_cast<const uint8_t*>(kt.chunk ? p.k : p.kp) + (px->g * (kD * 2) + lane * 16);
         copy_rows(mine, base, pitch, item + (lane >> 3) * kKBlk, 32, lw, 2, 0, 1);
       };
-      // e4m3: the next tile's raw rows wait in registers, 16 lanes per row.
-      uint4 raw[kE4M3 ? 16 : 1];
-      uint32_t ex = kNoExp;                    // of the row this lane looked up
-      auto fetch = [&](int idx) {
-        if constexpr (kE4M3) {
-          if (idx >= px->it0 + px->n) return;
-          const KeyTile kt = key_tile(*px, idx);
-          if (kt.chunk) return;
-          const int mine = slot_of(p, kt.tile * kBN + my_row, page, bad);
+      // e4m3: what is under way for the next tile: this lane's row's slot (lanes
+      // 0-15: first half) and exponent.
+      int slot_n = -1;
+      uint32_t ex_n = kNoExp, asked[2] = {0u, 0u};
+      auto fetch = [&](int idx, int h) {
+        if (!kE4M3 || idx >= px->it0 + px->n) return;
+        const KeyTile kt = key_tile(*px, idx);
+        if (kt.chunk) return;
+        if (h == 0) {
+          const int at = kt.tile * kBN + my_row;
+          slot_n = slot_of(p, at, page, bad);
           page = peek(idx + 1, my_row, 0);
-          ex = row_exp(p, p.ke, mine, px->g);
-          fetch_rows<16>(p, p.kp, piece16 * 16, px->g, raw,
-                         [&](int it) { return __shfl_sync(0xffffffffu, mine, it * 2 + sub16); });
-
+          ex_n = row_exp(p, p.ke, row_seen(p, *px, at) ? slot_n : -1, px->g);
         }
+        fetch_raw(&p.map_k, h, 32, 16 * h, 0, slot_n);
+        ++asked[h];
       };
       while ((px = next_segment()) != nullptr) {
         const int i0 = px->it0, n = px->n;
         if (n == 0) continue;
         page = peek(i0, my_row, tma_row);
-        fetch(i0);
+        fetch(i0, 0);
+        fetch(i0, 1);
         // Q: 32 lanes per row; rows past the unit's last token are zeros.
         ok = acquire(&sm.q_empty, nq);
         ++nq;
@@ -942,16 +974,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             push(full);
             if (kE4M3 || idx == i0) flush();   // the first tile is waited for
           } else {
-            if constexpr (kE4M3)
-              put_rows<16>(item, lw * 2 + sub16, 4, piece16, sub16, 2, raw, ex);
+            const uint32_t ex = ex_n;
+#pragma unroll 1
+            for (int h = 0; h < 2 && ok; ++h) {
+              ok = convert(h, kD, item + h * 32 * 128, lw * 2 + sub16, 4, piece16, 16 * h + sub16, 2, ex);
+              if (ok) fetch(idx + 1, h);
+            }
+            if (!ok) break;
             signal(full);
             if (n_pend > 0) flush();           // Q
           }
-          fetch(idx + 1);
         }
         flush();
       }
       land(sm.k_full, kNK, uk);
+      land_raw(0, asked);
     } else {
       const uint32_t vring_u = smem_u32(vring);
       const int my_row = kE4M3 ? row8 : row16;
@@ -968,20 +1005,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         copy_rows(mine, base, pitch, item + (ch >> 3) * kKBlk, 16, lw * 2 + (lane >> 4), 4,
                   lane >> 4, 2);
       };
-      uint4 raw[2][kE4M3 ? 8 : 1];
-      uint32_t ex[2] = {kNoExp, kNoExp};
+      uint32_t ex0 = kNoExp, ex1 = kNoExp, asked[2] = {0u, 0u};   // e4m3: exponents under way
       auto fetch = [&](int idx, int h) {
-        if constexpr (kE4M3) {
-          if (idx >= px->it0 + px->n) return;
-          const KeyTile kt = key_tile(*px, idx);
-          if (kt.chunk) return;
-          const int mine = slot_of(p, kt.tile * kBN + 64 * h + my_row, h ? page1 : page0, bad);
-          (h ? page1 : page0) = peek(idx + 1, 64 * h + my_row, 0);
-          ex[h] = row_exp(p, p.ve, mine, px->g);
-          fetch_rows<8>(p, p.vp, (int)rank * 128 + piece8 * 16, px->g, raw[h],
-                        [&](int it) { return __shfl_sync(0xffffffffu, mine, it * 4 + sub8); });
-
-        }
+        if (!kE4M3 || idx >= px->it0 + px->n) return;
+        const KeyTile kt = key_tile(*px, idx);
+        if (kt.chunk) return;
+        const int at = kt.tile * kBN + 64 * h + my_row;
+        const int slot = slot_of(p, at, h ? page1 : page0, bad);
+        const int next = peek(idx + 1, 64 * h + my_row, 0);
+        const uint32_t e = row_exp(p, p.ve, row_seen(p, *px, at) ? slot : -1, px->g);
+        page0 = h ? page0 : next;
+        page1 = h ? next : page1;
+        ex0 = h ? ex0 : e;
+        ex1 = h ? e : ex1;
+        fetch_raw(&p.map_v, 2 + h, 64, 0, (int)rank * 128, slot);
+        ++asked[h];
       };
       while ((px = next_segment()) != nullptr) {
         const int i0 = px->it0, n = px->n;
@@ -992,7 +1030,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fetch(i0, 1);
         for (int idx = i0; idx < i0 + n && ok; ++idx) {
           const KeyTile kt = key_tile(*px, idx);
-#pragma unroll(kE4M3 ? 2 : 1)
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             const int s = (int)(uv % kNV);
             const uint32_t item = vring_u + s * kVItem;
@@ -1015,16 +1053,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               copy_v(kt, h, item);
               push(full);
             } else {
-              if constexpr (kE4M3)
-                put_rows<8>(item, lw * 4 + sub8, 8, piece8, sub8, 4, raw[h], ex[h]);
+              ok = convert(2 + h, 128, item, lw * 4 + sub8, 8, piece8, sub8, 4, h ? ex1 : ex0);
+              if (!ok) break;
               signal(full);
+              fetch(idx + 1, h);
             }
-            fetch(idx + 1, h);
           }
         }
         flush();
       }
       land(sm.v_full, kNV, uv);
+      land_raw(2, asked);
     }
     if (bad) record_status(ctl, kStatusArg);
   } else {
@@ -1359,27 +1398,33 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-template <bool kE4M3, class L>
+template <bool kE4M3>
 cudaError_t launch(PagedTcParams& p, const DevCtl& ctl, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(
-      paged_tc_kernel<kE4M3, L>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+      paged_tc_kernel<kE4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   if (e != cudaSuccess) return e;
-  p.smem_bytes = min(layout_bytes<L>(p.Sq) + 1024, kSmemLimit);
-  return launch_pdl(paged_tc_kernel<kE4M3, L>, dim3(2 * p.n_clusters), dim3(kThreads),
+  p.smem_bytes = kSmemLimit;
+  return launch_pdl(paged_tc_kernel<kE4M3>, dim3(2 * p.n_clusters), dim3(kThreads),
                     (size_t)p.smem_bytes, st, p, ctl);
 }
 
-// A pool [slots][Hkv][256] bf16 as (64, slots, 4 Hkv column blocks).
-bool encode_pool(CUtensorMap* map, const void* base, const PagedParams& p, uint32_t box_blocks) {
+// bf16: a pool [slots][Hkv][256] as (64, slots, 4 Hkv column blocks), boxes of a
+// page's rows (64 at most) by `blocks` column blocks, or one for small pages.
+// e4m3: as (256 bytes, slots, Hkv), boxes of `rows` rows at most by `cols` bytes.
+bool encode_pool(CUtensorMap* map, const void* base, const PagedParams& p, uint32_t blocks,
+                 uint32_t rows, uint32_t cols) {
   auto fn = encode_fn();
   if (!fn) return false;
-  const uint32_t rows = 1u << p.page_shift;
-  cuuint64_t dims[3] = {64, (cuuint64_t)p.num_pages << p.page_shift, 4 * (cuuint64_t)p.Hkv};
-  cuuint64_t strides[2] = {(cuuint64_t)p.Hkv * kD * 2, 128};
-  cuuint32_t box[3] = {64, rows < 64 ? rows : 64, rows < 64 ? 1 : box_blocks};
+  const bool e4 = p.cache_dtype == kCacheE4M3;
+  const uint32_t page = 1u << p.page_shift, n = page < rows ? page : rows;
+  const cuuint64_t slots = (cuuint64_t)p.num_pages << p.page_shift, row = e4 ? kD : 2 * kD;
+  cuuint64_t dims[3] = {e4 ? (cuuint64_t)kD : 64, slots, (e4 ? 1 : 4) * (cuuint64_t)p.Hkv};
+  cuuint64_t strides[2] = {row * p.Hkv, e4 ? (cuuint64_t)kD : 128};
+  cuuint32_t box[3] = {e4 ? cols : 64, n, e4 || page < 64 ? 1 : blocks};
   cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return fn(map, e4 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            e4 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1413,8 +1458,10 @@ size_t paged_tc_workspace_bytes(const PagedParams& p) {
   const long long units = (long long)p.Hkv * ((p.Sq + kRowsTile / G - 1) / (kRowsTile / G));
   // The last group of sequences is the smallest: it decides.
   const int last = p.B % group ? p.B % group : group;
-  if (!may_cut(last * units, slots())) return 0;
-  return (size_t)slots() * 2 * kRowsTile * (kD + 2) * sizeof(float);
+  size_t n = 0;
+  if (may_cut(last * units, slots())) n += (size_t)slots() * 2 * kRowsTile * (kD + 2) * sizeof(float);
+  if (p.Sq > kSmemTokens) n += (size_t)slots() * 2 * pad_tokens(p.Sq) * sizeof(uint16_t);
+  return n;
 }
 
 cudaError_t launch_paged_tc(const PagedParams& a, float* ws, const DevCtl& ctl, cudaStream_t st) {
@@ -1426,22 +1473,23 @@ cudaError_t launch_paged_tc(const PagedParams& a, float* ws, const DevCtl& ctl, 
   p.tok_per_tile = kRowsTile / p.G;
   p.n_tiles = (a.Sq + p.tok_per_tile - 1) / p.tok_per_tile;
   p.scale_log2 = a.scale * 1.4426950408889634f;
-  p.use_tma = a.cache_dtype == kCacheBF16 && a.num_pages > 0;
-  if (p.use_tma && (!encode_pool(&p.map_k, a.kp, a, 4) || !encode_pool(&p.map_v, a.vp, a, 2)))
+  p.use_tma = a.num_pages > 0;
+  const bool e4 = a.cache_dtype == kCacheE4M3;
+  if (p.use_tma && (!encode_pool(&p.map_k, a.kp, a, 4, e4 ? 32 : 64, 256) ||
+                    !encode_pool(&p.map_v, a.vp, a, 2, 64, 128)))
     return cudaErrorUnknown;
   const int group = group_size(a);
+  const long long unit_tiles = (long long)a.Hkv * p.n_tiles;
+  const bool any_cut = may_cut((a.B % group ? a.B % group : group) * unit_tiles, slots());
+  p.codes = reinterpret_cast<uint16_t*>(
+      ws + (any_cut ? (size_t)slots() * 2 * kRowsTile * (kD + 2) : 0));
   for (int b0 = 0; b0 < a.B; b0 += group) {
     p.b0 = b0;
     p.nb = min(group, a.B - b0);
     const long long n_units = (long long)p.nb * a.Hkv * p.n_tiles;
     p.may_cut = may_cut(n_units, slots()) ? 1 : 0;
     p.n_clusters = p.may_cut ? slots() : (int)min(n_units, (long long)slots());
-    const bool e4 = a.cache_dtype == kCacheE4M3;
-    const bool short_s = a.Sq <= LayoutShort::kMaxTok;
-    const cudaError_t e = e4 ? (short_s ? launch<true, LayoutShort>(p, ctl, st)
-                                        : launch<true, LayoutLong>(p, ctl, st))
-                             : (short_s ? launch<false, LayoutShort>(p, ctl, st)
-                                        : launch<false, LayoutLong>(p, ctl, st));
+    const cudaError_t e = e4 ? launch<true>(p, ctl, st) : launch<false>(p, ctl, st);
     if (e != cudaSuccess) return e;
     if (p.may_cut) {
       const dim3 grid((unsigned)n_units, kRowsTile / 32);
