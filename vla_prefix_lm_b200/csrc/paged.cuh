@@ -43,20 +43,25 @@ __device__ __forceinline__ float exp_scale(uint32_t byte) {
                    : byte == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte << 23);
 }
 
-// Four raw e4m3 -> two bf16x2 words, times 2^(byte - 127), exact.  The byte's
-// exponent and mantissa moved to bf16's places read as the value times 2^-120
-// (subnormals too); the multiplication by m = 2^(byte - 7) undoes that and applies
-// the scale.  Integer and fp16-pipe instructions only: the conversion
-// instructions run at a quarter of their rate, on the units that the softmax's
-// exponentials need (7600 cycles a tile with them, 3 times the MMAs' time).
-__device__ __forceinline__ uint2 dequant4(uint32_t w, uint32_t m) {
-  uint2 o;
-  const uint32_t x0 = __byte_perm(w, 0u, 0x1404), x1 = __byte_perm(w, 0u, 0x3424);
-  const uint32_t y0 = ((x0 >> 4) & 0x07f007f0u) | (x0 & 0x80008000u);
-  const uint32_t y1 = ((x1 >> 4) & 0x07f007f0u) | (x1 & 0x80008000u);
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.x) : "r"(y0), "r"(m));
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.y) : "r"(y1), "r"(m));
+// e4m3 -> bf16, exact.  A byte's exponent and mantissa moved to bf16's places
+// read as the value times 2^-120 (subnormals too); a multiplication by 2^(byte - 7)
+// undoes that and applies the vector's scale.  The move: bytes spread to the low
+// half of each 16 bits, x; then 16 x + 240 (x & 0x80) has the sign at bit 15 and the
+// rest from bit 4 on.  The factors come as kernel parameters, so that they stay
+// multiply-adds: those, the byte permutes and the multiplication spread over
+// different pipes, whereas the conversion instructions run at a quarter of their
+// rate on the units that the softmax's exponentials need.
+struct Spread { uint32_t k16, k240; };
+__device__ __forceinline__ uint32_t spread_bf16(uint32_t x, uint32_t m, const Spread& k) {
+  const uint32_t y = x * k.k16 + (x & 0x00800080u) * k.k240;
+  uint32_t o;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(y), "r"(m));
   return o;
+}
+// Four bytes -> two bf16x2 words in order, times m.
+__device__ __forceinline__ uint2 dequant4(uint32_t w, uint32_t m, const Spread& k) {
+  return make_uint2(spread_bf16(__byte_perm(w, 0u, 0x4140), m, k),
+                    spread_bf16(__byte_perm(w, 0u, 0x4342), m, k));
 }
 // bf16x2 of 2^(byte - 7) twice (at most 2^127: rest_scale has what is missing);
 // NaN for byte 255, 0 where there is no row.
@@ -75,16 +80,11 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return o;
 }
 
-// The same for a transposed pair: bytes (key 0: d 0, d 1; key 1: d 0, d 1) ->
-// words (key 0, key 1) of d 0 and of d 1, times m's halves for the two keys.
-__device__ __forceinline__ uint2 dequant4_t(uint32_t w, uint32_t m) {
-  uint2 o;
-  const uint32_t x0 = __byte_perm(w, 0u, 0x2404), x1 = __byte_perm(w, 0u, 0x3414);
-  const uint32_t y0 = ((x0 >> 4) & 0x07f007f0u) | (x0 & 0x80008000u);
-  const uint32_t y1 = ((x1 >> 4) & 0x07f007f0u) | (x1 & 0x80008000u);
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.x) : "r"(y0), "r"(m));
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.y) : "r"(y1), "r"(m));
-  return o;
+// A transposed pair: bytes (key 0: d 0, d 1; key 1: d 0, d 1) -> words (key 0, key 1)
+// of d 0 and of d 1, times m's halves for the two keys.
+__device__ __forceinline__ uint2 dequant4_t(uint32_t w, uint32_t m, const Spread& k) {
+  return make_uint2(spread_bf16(__byte_perm(w, 0u, 0x4240), m, k),
+                    spread_bf16(__byte_perm(w, 0u, 0x4341), m, k));
 }
 
 // Writing to and reading from the pages (cache.cu).
@@ -194,6 +194,7 @@ struct PagedTcParams : PagedParams {
   int may_cut;               // units may be cut (ws is given)
   int smem_bytes;
   float scale_log2;
+  Spread spread;             // {16, 240}
 };
 bool paged_tc_applies(const PagedParams& p);
 size_t paged_tc_workspace_bytes(const PagedParams& p);
@@ -209,6 +210,7 @@ struct PagedDecodeParams : PagedParams {
   int b0, nb;                // this launch's sequences
   int n_ctas;
   float scale_log2;
+  Spread spread;             // {16, 240}
 };
 bool paged_decode_applies(const PagedParams& p);
 size_t paged_decode_workspace_bytes(const PagedParams& p);

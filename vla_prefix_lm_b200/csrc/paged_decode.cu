@@ -527,8 +527,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
           // after
           uint32_t r[4];
           ldsm_x4_t(vl + (n >> 3) * (kTile * 128) + ((((n & 7) + (lane >> 4)) ^ ks) << 4), r);
-          const uint2 a = dequant4_t(r[0], m_lo), e = dequant4_t(r[1], m_hi);
-          const uint2 f = dequant4_t(r[2], m_lo), w = dequant4_t(r[3], m_hi);
+          const uint2 a = dequant4_t(r[0], m_lo, p.spread), e = dequant4_t(r[1], m_hi, p.spread);
+          const uint2 f = dequant4_t(r[2], m_lo, p.spread), w = dequant4_t(r[3], m_hi, p.spread);
           mma16816(o[n], a.x, a.y, e.x, e.y, pb_lo, pb_hi);
           mma16816(o[n + 1], f.x, f.y, w.x, w.y, pb_lo, pb_hi);
         }
@@ -778,6 +778,7 @@ cudaError_t launch_paged_decode(const PagedParams& a, float* ws, const DevCtl& c
   p.G = a.Hq / a.Hkv;
   p.g_shift = p.G == 1 ? 0 : p.G == 2 ? 1 : p.G == 4 ? 2 : 3;
   p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.spread = {16u, 240u};
   const bool e4 = a.cache_dtype == kCacheE4M3;
   if (!encode_pool(&p.map_k, a.kp, a, e4) || !encode_pool(&p.map_v, a.vp, a, e4))
     return cudaErrorUnknown;

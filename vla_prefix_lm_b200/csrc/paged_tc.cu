@@ -43,6 +43,7 @@
 //   warp 13      PV issue (even CTA)
 //   warp 14      scheduler: derives the segments this cluster runs and hands
 //                them to the other warps through a two-entry ring
+//   warp 15      e4m3 pages: issues the raw rows' copies
 // TMEM per CTA (512 columns): O fp32 [0,256) | S0 [256,384) | S1 [384,512).
 // Shared memory per CTA: Q 64 KB | K ring 2 x 32 KB | V ring 4 x 16 KB, or 2 and
 // 32 KB of raw e4m3 rows | P 32 KB (also the output staging area) | control | codes
@@ -81,7 +82,7 @@ constexpr uint32_t kIdescPV = idesc_bf16_f32(2 * kBM, kD, false, true);
 constexpr uint32_t kColO = 0, kColS = 256;
 constexpr int kGroup = kPagedTcGroup;
 constexpr int kSegs = 2;                     // segment ring
-constexpr int kSegUsers = 14;                // warps that read it
+constexpr int kSegUsers = 14;                // warps that read it (e4m3: warp 15 too)
 
 
 // A run of key tiles of one unit on this cluster.
@@ -565,7 +566,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 4; ++s) mbar_init(&sm.pair[s], 2);
     for (int s = 0; s < kSegs; ++s) {
       mbar_init(&sm.seg_full[s], 1);
-      mbar_init(&sm.seg_empty[s], kSegUsers);
+      mbar_init(&sm.seg_empty[s], kSegUsers + (kE4M3 ? 1 : 0));
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&sm.raw_full[s], 1);
@@ -720,6 +721,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++n_seg;
         if (done) break;
       }
+    } else if (kE4M3) {
+      // --------------------------- warp 15: the raw halves of e4m3 tiles
+      // Lane r < 4 feeds half r (K 0, 1; V 2, 3) as soon as it has been read.  All
+      // rows come of every page that holds a row some query sees, zeros for others
+      // (a coordinate past the pool); a row that nobody sees gets scale 0, and every
+      // byte dequantises to a finite number.
+      const int rows = lane < 2 ? 32 : 64, b = min(1 << p.page_shift, rows), boxes = rows / b;
+      const int first = lane < 2 ? 64 * (int)rank + 32 * lane : 64 * (lane & 1);
+      const int past = p.num_pages << p.page_shift;
+      const CUtensorMap* map = lane < 2 ? &p.map_k : &p.map_v;
+      const int x = lane < 2 ? 0 : (int)rank * 128;
+      const uint32_t dst = smem_u32(smem + L::kOffRaw) + (lane & 3) * kRawHalf;
+      uint64_t* const full = &sm.raw_full[lane & 3];
+      uint32_t fills = 0;
+      while (const Segment* px = next_segment()) {
+        int idx = px->it0;
+        const int end = lane < 4 && p.use_tma ? min(px->it0 + px->n, px->n_cached) : 0;
+        int page[4];                          // of the next tile's boxes, loaded a tile ahead
+        auto peek = [&]() {
+          if (idx >= end) return;
+          const int at = key_tile(*px, idx).tile * kBN + first;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) page[i] = i < boxes ? page_seen(p, *px, at + i * b) : kNoRow;
+        };
+        peek();
+        long long t0 = clock64();
+        while (__any_sync(0xffffffffu, idx < end)) {
+          const bool ready =
+              idx < end && (fills == 0 || mbar_test_wait(&sm.raw_empty[lane & 3], (fills - 1) & 1));
+          if (ready) {
+            const int at = key_tile(*px, idx).tile * kBN + first;
+            mbar_arrive_expect_tx(full, kRawHalf);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (i < boxes) {
+                bool bad = false;             // (the loaders record it)
+                const int slot = slot_of(p, at + i * b, page[i], bad);
+                tma_load_3d_at(dst + i * b * (lane < 2 ? 256 : 128), map, full, x,
+                               slot < 0 ? past : slot, px->g);
+              }
+            }
+            ++fills;
+            ++idx;
+            peek();
+          }
+          if (__any_sync(0xffffffffu, ready)) {
+            t0 = clock64();
+          } else {
+            const bool late = (unsigned long long)(clock64() - t0) > ctl.wait_limit;
+            if (__any_sync(0xffffffffu, late || *(volatile int*)&sm.abort != 0)) {
+              if (*(volatile int*)&sm.abort == 0) {
+                record_status(ctl, kStatusTimeout);
+                *(volatile int*)&sm.abort = 1;
+              }
+              ok = false;
+              break;
+            }
+          }
+        }
+      }
+      // A bounded wait for the last copies.
+      if (lane < 4 && fills > 0) (void)mbar_wait(full, (fills - 1) & 1, ctl);
+      __syncwarp();
     }
   } else if (warp >= 8) {
     // ---------------------------------------------------------- loaders
@@ -797,23 +861,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool tma = p.use_tma && whole_tile(p, *px, kt);
       return page_of(p, *px, at + (tma ? tma_row : row));
     };
-    // e4m3.  Raw halves come by TMA, a tile ahead of their use, all rows of every
-    // page that holds a row some query sees; rows that nobody sees get scale 0
-    // (every byte dequantises to a finite number).  r: raw half (K 0, 1; V 2, 3).
-    uint8_t* const raw = smem + L::kOffRaw;
-    uint32_t raw_n[2] = {0u, 0u};             // fills of this operand's halves
-    auto fetch_raw = [&](const CUtensorMap* map, int r, int rows, int slot_lane, int x, int slot) {
-      if (lw != 0 || !p.use_tma) return;      // slot: of the row this lane looked up
-      const int b = min(1 << p.page_shift, rows), n = rows / b;
-      const int first = __shfl_sync(0xffffffffu, slot, slot_lane + min(lane, n - 1) * (b >> 1));
-      const uint32_t fills = raw_n[r & 1];
-      if (fills > 0) (void)warp_wait(&sm.raw_empty[r], (fills - 1) & 1, sm, ctl);
-      if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[r], kRawHalf);
-      __syncwarp();
-      if (lane < n)
-        tma_load_3d_at(smem_u32(raw + r * kRawHalf + lane * b * (kRawHalf / rows)), map,
-                       &sm.raw_full[r], x, first < 0 ? p.num_pages << p.page_shift : first, px->g);
-    };
+    uint8_t* const raw = smem + L::kOffRaw;   // e4m3: filled by warp 15
+    uint32_t raw_n[2] = {0u, 0u};             // fills of this operand's halves used up
     // A raw half -> bf16 rows of an item.  16 lanes (K) or 8 (V) per row; each
     // eight lanes hold four 16-byte pieces (c16 ..) of two adjacent rows, whose
     // bf16 chunks fall on eight different bank groups.  Lane: pieces of rows row0 +
@@ -836,8 +885,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int it = 0; it < 8; it += 2) {
         const uint32_t ma = __shfl_sync(0xffffffffu, m, lane0 + it * lstep);
         const uint32_t mb = __shfl_sync(0xffffffffu, m, lane0 + (it + 1) * lstep);
-        uint2 qa[4] = {dequant4(wa.x, ma), dequant4(wa.y, ma), dequant4(wa.z, ma), dequant4(wa.w, ma)};
-        uint2 qb[4] = {dequant4(wb.x, mb), dequant4(wb.y, mb), dequant4(wb.z, mb), dequant4(wb.w, mb)};
+        uint2 qa[4] = {dequant4(wa.x, ma, p.spread), dequant4(wa.y, ma, p.spread), dequant4(wa.z, ma, p.spread), dequant4(wa.w, ma, p.spread)};
+        uint2 qb[4] = {dequant4(wb.x, mb, p.spread), dequant4(wb.y, mb, p.spread), dequant4(wb.z, mb, p.spread), dequant4(wb.w, mb, p.spread)};
         src += 2 * step * row_bytes;
         if (it < 6) {
           wa = ld_shared_v4(src);
@@ -866,13 +915,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&sm.raw_empty[r]);   // the half has been read
       ++raw_n[r & 1];
       return true;
-    };
-    // After the last use: a bounded wait for raw halves still on their way.
-    auto land_raw = [&](int r0, const uint32_t (&asked)[2]) {
-      if (kE4M3 && p.use_tma && lw == 0 && lane == 0)
-        for (int h = 0; h < 2; ++h)
-          if (asked[h] > 0) (void)mbar_wait(&sm.raw_full[r0 + h], (asked[h] - 1) & 1, ctl);
-      __syncwarp();
     };
     const int odd = (lane >> 2) & 1;
     const int sub16 = odd, piece16 = (lane & 3) + 4 * (lane >> 3);
@@ -914,29 +956,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             static_cast<const uint8_t*>(kt.chunk ? p.k : p.kp) + (px->g * (kD * 2) + lane * 16);
         copy_rows(mine, base, pitch, item + (lane >> 3) * kKBlk, 32, lw, 2, 0, 1);
       };
-      // e4m3: what is under way for the next tile: this lane's row's slot (lanes
-      // 0-15: first half) and exponent.
-      int slot_n = -1;
-      uint32_t ex_n = kNoExp, asked[2] = {0u, 0u};
-      auto fetch = [&](int idx, int h) {
+      uint32_t ex_n = kNoExp;                  // e4m3: this lane's row's exponent, next tile
+      auto fetch = [&](int idx) {
         if (!kE4M3 || idx >= px->it0 + px->n) return;
         const KeyTile kt = key_tile(*px, idx);
         if (kt.chunk) return;
-        if (h == 0) {
-          const int at = kt.tile * kBN + my_row;
-          slot_n = slot_of(p, at, page, bad);
-          page = peek(idx + 1, my_row, 0);
-          ex_n = row_exp(p, p.ke, row_seen(p, *px, at) ? slot_n : -1, px->g);
-        }
-        fetch_raw(&p.map_k, h, 32, 16 * h, 0, slot_n);
-        ++asked[h];
+        const int at = kt.tile * kBN + my_row;
+        const int slot = slot_of(p, at, page, bad);
+        page = peek(idx + 1, my_row, 0);
+        ex_n = row_exp(p, p.ke, row_seen(p, *px, at) ? slot : -1, px->g);
       };
       while ((px = next_segment()) != nullptr) {
         const int i0 = px->it0, n = px->n;
         if (n == 0) continue;
         page = peek(i0, my_row, tma_row);
-        fetch(i0, 0);
-        fetch(i0, 1);
+        fetch(i0);
         // Q: 32 lanes per row; rows past the unit's last token are zeros.
         ok = acquire(&sm.q_empty, nq);
         ++nq;
@@ -975,11 +1009,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (kE4M3 || idx == i0) flush();   // the first tile is waited for
           } else {
             const uint32_t ex = ex_n;
+            fetch(idx + 1);
 #pragma unroll 1
-            for (int h = 0; h < 2 && ok; ++h) {
+            for (int h = 0; h < 2 && ok; ++h)
               ok = convert(h, kD, item + h * 32 * 128, lw * 2 + sub16, 4, piece16, 16 * h + sub16, 2, ex);
-              if (ok) fetch(idx + 1, h);
-            }
             if (!ok) break;
             signal(full);
             if (n_pend > 0) flush();           // Q
@@ -988,7 +1021,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         flush();
       }
       land(sm.k_full, kNK, uk);
-      land_raw(0, asked);
     } else {
       const uint32_t vring_u = smem_u32(vring);
       const int my_row = kE4M3 ? row8 : row16;
@@ -1005,7 +1037,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         copy_rows(mine, base, pitch, item + (ch >> 3) * kKBlk, 16, lw * 2 + (lane >> 4), 4,
                   lane >> 4, 2);
       };
-      uint32_t ex0 = kNoExp, ex1 = kNoExp, asked[2] = {0u, 0u};   // e4m3: exponents under way
+      uint32_t ex0 = kNoExp, ex1 = kNoExp;     // e4m3: exponents, next half items
       auto fetch = [&](int idx, int h) {
         if (!kE4M3 || idx >= px->it0 + px->n) return;
         const KeyTile kt = key_tile(*px, idx);
@@ -1018,8 +1050,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         page1 = h ? next : page1;
         ex0 = h ? ex0 : e;
         ex1 = h ? e : ex1;
-        fetch_raw(&p.map_v, 2 + h, 64, 0, (int)rank * 128, slot);
-        ++asked[h];
       };
       while ((px = next_segment()) != nullptr) {
         const int i0 = px->it0, n = px->n;
@@ -1053,17 +1083,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               copy_v(kt, h, item);
               push(full);
             } else {
-              ok = convert(2 + h, 128, item, lw * 4 + sub8, 8, piece8, sub8, 4, h ? ex1 : ex0);
+              const uint32_t ex = h ? ex1 : ex0;
+              fetch(idx + 1, h);
+              ok = convert(2 + h, 128, item, lw * 4 + sub8, 8, piece8, sub8, 4, ex);
               if (!ok) break;
               signal(full);
-              fetch(idx + 1, h);
             }
           }
         }
         flush();
       }
       land(sm.v_full, kNV, uv);
-      land_raw(2, asked);
     }
     if (bad) record_status(ctl, kStatusArg);
   } else {
@@ -1473,6 +1503,7 @@ cudaError_t launch_paged_tc(const PagedParams& a, float* ws, const DevCtl& ctl, 
   p.tok_per_tile = kRowsTile / p.G;
   p.n_tiles = (a.Sq + p.tok_per_tile - 1) / p.tok_per_tile;
   p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.spread = {16u, 240u};
   p.use_tma = a.num_pages > 0;
   const bool e4 = a.cache_dtype == kCacheE4M3;
   if (p.use_tma && (!encode_pool(&p.map_k, a.kp, a, 4, e4 ? 32 : 64, 256) ||
