@@ -43,7 +43,6 @@
 //   warp 13      PV issue (even CTA)
 //   warp 14      scheduler: derives the segments this cluster runs and hands
 //                them to the other warps through a two-entry ring
-//   warp 15      e4m3 pages: issues the raw rows' copies
 // TMEM per CTA (512 columns): O fp32 [0,256) | S0 [256,384) | S1 [384,512).
 // Shared memory per CTA: Q 64 KB | K ring 2 x 32 KB | V ring 4 x 16 KB, or 2 and
 // 32 KB of raw e4m3 rows | P 32 KB (also the output staging area) | control | codes
@@ -82,7 +81,7 @@ constexpr uint32_t kIdescPV = idesc_bf16_f32(2 * kBM, kD, false, true);
 constexpr uint32_t kColO = 0, kColS = 256;
 constexpr int kGroup = kPagedTcGroup;
 constexpr int kSegs = 2;                     // segment ring
-constexpr int kSegUsers = 14;                // warps that read it (e4m3: warp 15 too)
+constexpr int kSegUsers = 14;                // warps that read it
 
 
 // A run of key tiles of one unit on this cluster.
@@ -99,15 +98,15 @@ struct Segment {
   int any_e;                 // an expert among the tokens
 };
 
-// bf16 pages: four V halves.  e4m3: two, and as much room for raw rows, half an
-// item each: K 2 x [32 keys x 256 bytes], V 2 x [64 keys x 128 bytes].
-constexpr int kRawHalf = 8192;
+// bf16 pages: four V halves.  e4m3: two, and as much room for raw rows: each loader
+// warp has two pieces, K of 16 keys x 256 bytes, V of 32 keys x 128 bytes.
+constexpr int kRawPiece = 4096;
 template <bool kE4M3>
 struct Layout {
   static constexpr int kNV = kE4M3 ? 2 : 4;
   static constexpr int kOffV = kOffK + kNK * kKItem;
   static constexpr int kOffRaw = kOffV + kNV * kVItem;
-  static constexpr int kOffP = kOffRaw + (kE4M3 ? 4 * kRawHalf : 0);
+  static constexpr int kOffP = kOffRaw + (kE4M3 ? 8 * kRawPiece : 0);
   static constexpr int kOffCtl = kOffP + kPBytes;
 };
 constexpr int kTiles = (kMaxTokens + kBN - 1) / kBN;
@@ -131,7 +130,7 @@ struct __align__(8) Smem {
   uint64_t drain_qk, drain_pv;
   uint64_t pair[4];                 // a quarter's two warps meet
   uint64_t seg_full[kSegs], seg_empty[kSegs];
-  uint64_t raw_full[4], raw_empty[4];   // e4m3: K halves, V halves (this CTA's)
+  uint64_t raw_full[8];             // e4m3: the loader warps' raw pieces
   uint32_t tmem_base;
   int abort;
   Plan plan;
@@ -509,6 +508,26 @@ __device__ __noinline__ void copy_rows(int mine, const uint8_t* base, uint32_t p
   }
 }
 
+// Where a lane's first 16 bytes lie in a raw piece: rows of 256 bytes (two a pass) or
+// 128 bytes (four a pass); a pass is 512 bytes.
+__device__ __forceinline__ uint32_t lane_src(int rows, int sub, int c16) {
+  return (uint32_t)(sub * (512 / rows) + c16 * 16);
+}
+// Multiplies the eight rebuilt pieces of a lane (see rebuild) by rest_scale.
+__device__ __noinline__ void rescale_rows(uint32_t base, int rows, uint32_t cs, int l0, uint32_t e) {
+  const uint32_t m = rest_scale(e);
+#pragma unroll 1
+  for (int it = 0; it < 8; ++it) {
+    const uint32_t r = __shfl_sync(0xffffffffu, m, l0 + it * rows);
+    const uint32_t a0 = base + it * rows * 128 + ((cs ^ ((it * rows) & 7)) << 4);
+    for (int k = 0; k < 2; ++k) {
+      uint4 w = ld_shared_v4(a0 ^ (16 * k));
+      w = make_uint4(mul_bf16x2(w.x, r), mul_bf16x2(w.y, r), mul_bf16x2(w.z, r), mul_bf16x2(w.w, r));
+      st_shared_v4(a0 ^ (16 * k), w);
+    }
+  }
+  __syncwarp();
+}
 // The exponent byte of row r, loaded by the lane that looked the row up.
 __device__ __forceinline__ uint32_t row_exp(const PagedTcParams& p, const uint8_t* exps, int r, int g) {
   return r >= 0 ? (uint32_t)__ldg(exps + (unsigned long long)(uint32_t)r * (uint32_t)p.Hkv + g) : kNoExp;
@@ -566,12 +585,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 4; ++s) mbar_init(&sm.pair[s], 2);
     for (int s = 0; s < kSegs; ++s) {
       mbar_init(&sm.seg_full[s], 1);
-      mbar_init(&sm.seg_empty[s], kSegUsers + (kE4M3 ? 1 : 0));
+      mbar_init(&sm.seg_empty[s], kSegUsers);
     }
-    for (int s = 0; s < 4; ++s) {
-      mbar_init(&sm.raw_full[s], 1);
-      mbar_init(&sm.raw_empty[s], 2);
-    }
+    for (int s = 0; s < 8; ++s) mbar_init(&sm.raw_full[s], 1);
     sm.abort = 0;
     fence_barrier_init();
   }
@@ -721,69 +737,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++n_seg;
         if (done) break;
       }
-    } else if (kE4M3) {
-      // --------------------------- warp 15: the raw halves of e4m3 tiles
-      // Lane r < 4 feeds half r (K 0, 1; V 2, 3) as soon as it has been read.  All
-      // rows come of every page that holds a row some query sees, zeros for others
-      // (a coordinate past the pool); a row that nobody sees gets scale 0, and every
-      // byte dequantises to a finite number.
-      const int rows = lane < 2 ? 32 : 64, b = min(1 << p.page_shift, rows), boxes = rows / b;
-      const int first = lane < 2 ? 64 * (int)rank + 32 * lane : 64 * (lane & 1);
-      const int past = p.num_pages << p.page_shift;
-      const CUtensorMap* map = lane < 2 ? &p.map_k : &p.map_v;
-      const int x = lane < 2 ? 0 : (int)rank * 128;
-      const uint32_t dst = smem_u32(smem + L::kOffRaw) + (lane & 3) * kRawHalf;
-      uint64_t* const full = &sm.raw_full[lane & 3];
-      uint32_t fills = 0;
-      while (const Segment* px = next_segment()) {
-        int idx = px->it0;
-        const int end = lane < 4 && p.use_tma ? min(px->it0 + px->n, px->n_cached) : 0;
-        int page[4];                          // of the next tile's boxes, loaded a tile ahead
-        auto peek = [&]() {
-          if (idx >= end) return;
-          const int at = key_tile(*px, idx).tile * kBN + first;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) page[i] = i < boxes ? page_seen(p, *px, at + i * b) : kNoRow;
-        };
-        peek();
-        long long t0 = clock64();
-        while (__any_sync(0xffffffffu, idx < end)) {
-          const bool ready =
-              idx < end && (fills == 0 || mbar_test_wait(&sm.raw_empty[lane & 3], (fills - 1) & 1));
-          if (ready) {
-            const int at = key_tile(*px, idx).tile * kBN + first;
-            mbar_arrive_expect_tx(full, kRawHalf);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (i < boxes) {
-                bool bad = false;             // (the loaders record it)
-                const int slot = slot_of(p, at + i * b, page[i], bad);
-                tma_load_3d_at(dst + i * b * (lane < 2 ? 256 : 128), map, full, x,
-                               slot < 0 ? past : slot, px->g);
-              }
-            }
-            ++fills;
-            ++idx;
-            peek();
-          }
-          if (__any_sync(0xffffffffu, ready)) {
-            t0 = clock64();
-          } else {
-            const bool late = (unsigned long long)(clock64() - t0) > ctl.wait_limit;
-            if (__any_sync(0xffffffffu, late || *(volatile int*)&sm.abort != 0)) {
-              if (*(volatile int*)&sm.abort == 0) {
-                record_status(ctl, kStatusTimeout);
-                *(volatile int*)&sm.abort = 1;
-              }
-              ok = false;
-              break;
-            }
-          }
-        }
-      }
-      // A bounded wait for the last copies.
-      if (lane < 4 && fills > 0) (void)mbar_wait(full, (fills - 1) & 1, ctl);
-      __syncwarp();
     }
   } else if (warp >= 8) {
     // ---------------------------------------------------------- loaders
@@ -844,11 +797,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     // Row lookup: lane l looks up the l-th of the 32 rows (of 64) that this warp
     // copies of an item; rows of 512 bytes take all 32 lanes, of 256 bytes 16
-    // lanes, of 128 bytes 8 lanes.  Page ids are loaded a tile ahead (peek), so
+    // lanes.  (e4m3: rows 32 lw + l.)  Page ids are loaded a tile ahead (peek), so
     // that their latency does not delay the copies.
     const int row32 = lane * 2 + lw;                               // 32 lanes per row
     const int row16 = (lane >> 1) * 4 + lw * 2 + (lane & 1);       // 16
-    const int row8 = (lane >> 2) * 8 + lw * 4 + (lane & 3);        // 8
     // TMA tiles: lane l has the page of box l.
     const int box = min(1 << p.page_shift, 64);                    // rows per box
     const int boxes = 64 / box;                                    // per 64 keys
@@ -861,64 +813,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool tma = p.use_tma && whole_tile(p, *px, kt);
       return page_of(p, *px, at + (tma ? tma_row : row));
     };
-    uint8_t* const raw = smem + L::kOffRaw;   // e4m3: filled by warp 15
-    uint32_t raw_n[2] = {0u, 0u};             // fills of this operand's halves used up
-    // A raw half -> bf16 rows of an item.  16 lanes (K) or 8 (V) per row; each
-    // eight lanes hold four 16-byte pieces (c16 ..) of two adjacent rows, whose
-    // bf16 chunks fall on eight different bank groups.  Lane: pieces of rows row0 +
-    // it * step, it < 8, exponent of row it in lane lane0 + it * lstep.
-    auto convert = [&](int r, int row_bytes, uint32_t item, int row0, int step, int c16, int lane0,
-                       int lstep, uint32_t e) -> bool {
-      const uint32_t fills = raw_n[r & 1];
-      if (p.use_tma && !warp_wait(&sm.raw_full[r], fills & 1, sm, ctl)) return false;
-      uint32_t src = smem_u32(raw + r * kRawHalf) + row0 * row_bytes + c16 * 16;
-      const uint32_t base = item + row0 * 128 + (c16 >> 2) * kKBlk;
-      const int c = (c16 & 3) * 2, x0 = row0 & 7, x1 = (row0 + step) & 7;
-      uint32_t a0 = base + ((c ^ x0) << 4), a1 = base + (((c + 1) ^ x0) << 4);
-      uint32_t b0 = base + step * 128 + ((c ^ x1) << 4);
-      uint32_t b1 = base + step * 128 + (((c + 1) ^ x1) << 4);
-      const uint32_t m = main_scale(e);
-      const bool rest = __any_sync(0xffffffffu, e > 134u && e < 255u);   // over 448 * 2^7
-      const uint32_t m2 = rest ? rest_scale(e) : 0u;
-      uint4 wa = ld_shared_v4(src), wb = ld_shared_v4(src + step * row_bytes);
-#pragma unroll 1
-      for (int it = 0; it < 8; it += 2) {
-        const uint32_t ma = __shfl_sync(0xffffffffu, m, lane0 + it * lstep);
-        const uint32_t mb = __shfl_sync(0xffffffffu, m, lane0 + (it + 1) * lstep);
-        uint2 qa[4] = {dequant4(wa.x, ma, p.spread), dequant4(wa.y, ma, p.spread), dequant4(wa.z, ma, p.spread), dequant4(wa.w, ma, p.spread)};
-        uint2 qb[4] = {dequant4(wb.x, mb, p.spread), dequant4(wb.y, mb, p.spread), dequant4(wb.z, mb, p.spread), dequant4(wb.w, mb, p.spread)};
-        src += 2 * step * row_bytes;
-        if (it < 6) {
-          wa = ld_shared_v4(src);
-          wb = ld_shared_v4(src + step * row_bytes);
-        }
-        if (rest) {
-          const uint32_t ra = __shfl_sync(0xffffffffu, m2, lane0 + it * lstep);
-          const uint32_t rb = __shfl_sync(0xffffffffu, m2, lane0 + (it + 1) * lstep);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            qa[i] = make_uint2(mul_bf16x2(qa[i].x, ra), mul_bf16x2(qa[i].y, ra));
-            qb[i] = make_uint2(mul_bf16x2(qb[i].x, rb), mul_bf16x2(qb[i].y, rb));
-          }
-        }
-        st_shared_v4(a0, make_uint4(qa[0].x, qa[0].y, qa[1].x, qa[1].y));
-        st_shared_v4(a1, make_uint4(qa[2].x, qa[2].y, qa[3].x, qa[3].y));
-        st_shared_v4(b0, make_uint4(qb[0].x, qb[0].y, qb[1].x, qb[1].y));
-        st_shared_v4(b1, make_uint4(qb[2].x, qb[2].y, qb[3].x, qb[3].y));
-        const uint32_t d = 2 * step * 128;    // (2 * step is a multiple of 8 rows)
-        a0 += d;
-        a1 += d;
-        b0 += d;
-        b1 += d;
+    // e4m3.  A warp copies (TMA) and rebuilds rows of its own, 32 of K or of a V half
+    // item, in two pieces: a piece's next copy starts as soon as it has been read and
+    // lands while the other is rebuilt.  All rows come of a page that holds a row
+    // some query sees, zeros for others (a coordinate past the pool); a row that
+    // nobody sees gets scale 0, and every byte dequantises to a finite number.
+    const uint32_t raw_u = smem_u32(smem + L::kOffRaw) + (warp - 8) * 2 * kRawPiece;
+    uint64_t* const raw_full = &sm.raw_full[(warp - 8) * 2];
+    uint32_t used = 0;                        // tiles whose pieces have been used up
+    // Piece h's copy: its rows, from the slots of lanes l0 and l0 + 16 (V in pages of
+    // 16 tokens: two boxes).
+    auto copy_raw = [&](const CUtensorMap* map, int h, int slot, int l0, int x, int bytes) {
+      if (!p.use_tma) return;
+      const int past = p.num_pages << p.page_shift;
+      const int s0 = __shfl_sync(0xffffffffu, slot, l0), s1 = __shfl_sync(0xffffffffu, slot, 16);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&raw_full[h], kRawPiece);
+        tma_load_3d_at(raw_u + h * kRawPiece, map, &raw_full[h], x, s0 < 0 ? past : s0, px->g);
+        if (bytes < kRawPiece)
+          tma_load_3d_at(raw_u + h * kRawPiece + bytes, map, &raw_full[h], x, s1 < 0 ? past : s1, px->g);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.raw_empty[r]);   // the half has been read
-      ++raw_n[r & 1];
+    };
+    // Rebuilds piece h into rows row0 .. of an item: a pass has `rows` rows (2 of K, 4
+    // of V), this lane 16 bytes (piece c16) of row `sub`; each eight lanes hold four
+    // pieces of two adjacent rows, whose bf16 chunks fall on eight different bank
+    // groups.  The exponent of row i sits in lane l0 + i.
+    auto rebuild = [&](int h, uint32_t item, int rows, int sub, int c16, int l0, uint32_t e) -> bool {
+      if (p.use_tma && !warp_wait(&raw_full[h], used & 1, sm, ctl)) return false;
+      const uint32_t src0 = raw_u + h * kRawPiece + lane_src(rows, sub, c16);
+      const uint32_t base = item + sub * 128 + (c16 >> 2) * kKBlk;
+      const uint32_t cs = (uint32_t)(((c16 & 3) * 2) ^ sub);     // chunk, swizzled by the row's low bits
+      const uint32_t m = main_scale(e);
+      uint4 wa = ld_shared_v4(src0), wb = ld_shared_v4(src0 + 512);
+#pragma unroll 1
+      for (int it = 0; it < 8; it += 2) {
+        const uint32_t ma = __shfl_sync(0xffffffffu, m, l0 + it * rows + sub);
+        const uint32_t mb = __shfl_sync(0xffffffffu, m, l0 + (it + 1) * rows + sub);
+        const uint2 qa[4] = {dequant4(wa.x, ma, p.spread), dequant4(wa.y, ma, p.spread),
+                             dequant4(wa.z, ma, p.spread), dequant4(wa.w, ma, p.spread)};
+        const uint2 qb[4] = {dequant4(wb.x, mb, p.spread), dequant4(wb.y, mb, p.spread),
+                             dequant4(wb.z, mb, p.spread), dequant4(wb.w, mb, p.spread)};
+        if (it < 6) {
+          wa = ld_shared_v4(src0 + (it + 2) * 512);
+          wb = ld_shared_v4(src0 + (it + 3) * 512);
+        }
+        const uint32_t ra = it * rows, rb = ra + rows;
+        const uint32_t a0 = base + ra * 128 + ((cs ^ (ra & 7)) << 4);
+        const uint32_t b0 = base + rb * 128 + ((cs ^ (rb & 7)) << 4);
+        st_shared_v4(a0, make_uint4(qa[0].x, qa[0].y, qa[1].x, qa[1].y));
+        st_shared_v4(a0 ^ 16, make_uint4(qa[2].x, qa[2].y, qa[3].x, qa[3].y));
+        st_shared_v4(b0, make_uint4(qb[0].x, qb[0].y, qb[1].x, qb[1].y));
+        st_shared_v4(b0 ^ 16, make_uint4(qb[2].x, qb[2].y, qb[3].x, qb[3].y));
+      }
+      __syncwarp();
+      // what scales above 2^7 (values above 448 * 2^7) lack
+      if (__any_sync(0xffffffffu, e > 134u && e < 255u))
+        rescale_rows(base, rows, cs, l0 + sub, e);
       return true;
     };
+    // After the last use: a bounded wait for pieces still on their way.
+    auto land_raw = [&](uint32_t asked) {
+      if (kE4M3 && p.use_tma && lane == 0 && asked > 0)
+        for (int h = 0; h < 2; ++h) (void)mbar_wait(&raw_full[h], (asked - 1) & 1, ctl);
+      __syncwarp();
+    };
     const int odd = (lane >> 2) & 1;
-    const int sub16 = odd, piece16 = (lane & 3) + 4 * (lane >> 3);
-    const int sub8 = odd + 2 * (lane >> 4), piece8 = (lane & 3) + 4 * ((lane >> 3) & 1);
+    const int sub2 = odd, piece2 = (lane & 3) + 4 * (lane >> 3);
+    const int sub4 = odd + 2 * (lane >> 4), piece4 = (lane & 3) + 4 * ((lane >> 3) & 1);
     // The boxes of one item: `blocks` 64-column blocks from block c0 of the
     // head, keys from position x0; lane l brings box l / blocks, block l % blocks
     // (pages of 64 tokens and more: one box of all blocks).  A page id out of
@@ -944,7 +906,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t pitch = (uint32_t)p.Hkv * (kD * 2);             // bf16 rows
     if (warp < 10) {
       const uint32_t kring_u = smem_u32(kring), sQ_u = smem_u32(sQ);
-      const int my_row = 64 * (int)rank + (kE4M3 ? row16 : row32);
+      const int my_row = 64 * (int)rank + (kE4M3 ? 32 * lw + lane : row32);
       const int tma_row = 64 * (int)rank + (boxes == 1 ? 0 : min(lane >> 2, boxes - 1) * box);
       uint32_t uk = 0, nq = 0;
       int page = kNoRow;
@@ -956,21 +918,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             static_cast<const uint8_t*>(kt.chunk ? p.k : p.kp) + (px->g * (kD * 2) + lane * 16);
         copy_rows(mine, base, pitch, item + (lane >> 3) * kKBlk, 32, lw, 2, 0, 1);
       };
-      uint32_t ex_n = kNoExp;                  // e4m3: this lane's row's exponent, next tile
+      // e4m3: this lane's row of the next tile, its slot (-1: no such tile) and exponent.
+      int slot_n = -1;
+      bool has_n = false;
+      uint32_t ex_n = kNoExp, asked = 0;
       auto fetch = [&](int idx) {
+        has_n = false;
         if (!kE4M3 || idx >= px->it0 + px->n) return;
         const KeyTile kt = key_tile(*px, idx);
         if (kt.chunk) return;
         const int at = kt.tile * kBN + my_row;
-        const int slot = slot_of(p, at, page, bad);
+        slot_n = slot_of(p, at, page, bad);
         page = peek(idx + 1, my_row, 0);
-        ex_n = row_exp(p, p.ke, row_seen(p, *px, at) ? slot : -1, px->g);
+        ex_n = row_exp(p, p.ke, row_seen(p, *px, at) ? slot_n : -1, px->g);
+        has_n = true;
+        ++asked;
       };
       while ((px = next_segment()) != nullptr) {
         const int i0 = px->it0, n = px->n;
         if (n == 0) continue;
         page = peek(i0, my_row, tma_row);
         fetch(i0);
+        if (has_n) {
+          copy_raw(&p.map_k, 0, slot_n, 0, 0, kRawPiece);
+          copy_raw(&p.map_k, 1, slot_n, 16, 0, kRawPiece);
+        }
         // Q: 32 lanes per row; rows past the unit's last token are zeros.
         ok = acquire(&sm.q_empty, nq);
         ++nq;
@@ -1011,8 +983,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t ex = ex_n;
             fetch(idx + 1);
 #pragma unroll 1
-            for (int h = 0; h < 2 && ok; ++h)
-              ok = convert(h, kD, item + h * 32 * 128, lw * 2 + sub16, 4, piece16, 16 * h + sub16, 2, ex);
+            for (int h = 0; h < 2 && ok; ++h) {
+              ok = rebuild(h, item + (32 * lw + 16 * h) * 128, 2, sub2, piece2, 16 * h, ex);
+              if (ok && has_n) copy_raw(&p.map_k, h, slot_n, 16 * h, 0, kRawPiece);
+            }
+            ++used;
             if (!ok) break;
             signal(full);
             if (n_pend > 0) flush();           // Q
@@ -1021,9 +996,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         flush();
       }
       land(sm.k_full, kNK, uk);
+      land_raw(asked);
     } else {
       const uint32_t vring_u = smem_u32(vring);
-      const int my_row = kE4M3 ? row8 : row16;
+      const int my_row = kE4M3 ? 32 * lw + lane : row16;
+      const int box_bytes = min(1 << p.page_shift, 32) * 128;      // e4m3: of a raw piece's boxes
       const int tma_row = boxes == 1 ? 0 : min(lane >> 1, boxes - 1) * box;
       uint32_t uv = 0;
       int page0 = kNoRow, page1 = kNoRow;
@@ -1037,27 +1014,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         copy_rows(mine, base, pitch, item + (ch >> 3) * kKBlk, 16, lw * 2 + (lane >> 4), 4,
                   lane >> 4, 2);
       };
-      uint32_t ex0 = kNoExp, ex1 = kNoExp;     // e4m3: exponents, next half items
-      auto fetch = [&](int idx, int h) {
-        if (!kE4M3 || idx >= px->it0 + px->n) return;
+      // e4m3: this lane's row of the next half item (false: none), its exponent.
+      uint32_t ex0 = kNoExp, ex1 = kNoExp, asked = 0;
+      int slot_n = -1;
+      auto fetch = [&](int idx, int h) -> bool {
+        if (!kE4M3 || idx >= px->it0 + px->n) return false;
         const KeyTile kt = key_tile(*px, idx);
-        if (kt.chunk) return;
+        if (kt.chunk) return false;
         const int at = kt.tile * kBN + 64 * h + my_row;
-        const int slot = slot_of(p, at, h ? page1 : page0, bad);
+        slot_n = slot_of(p, at, h ? page1 : page0, bad);
         const int next = peek(idx + 1, 64 * h + my_row, 0);
-        const uint32_t e = row_exp(p, p.ve, row_seen(p, *px, at) ? slot : -1, px->g);
+        const uint32_t e = row_exp(p, p.ve, row_seen(p, *px, at) ? slot_n : -1, px->g);
         page0 = h ? page0 : next;
         page1 = h ? next : page1;
         ex0 = h ? ex0 : e;
         ex1 = h ? e : ex1;
+        asked += h;
+        return true;
       };
       while ((px = next_segment()) != nullptr) {
         const int i0 = px->it0, n = px->n;
         if (n == 0) continue;
         page0 = peek(i0, my_row, tma_row);
         page1 = peek(i0, 64 + my_row, 64 + tma_row);
-        fetch(i0, 0);
-        fetch(i0, 1);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h)
+          if (fetch(i0, h)) copy_raw(&p.map_v, h, slot_n, 0, (int)rank * 128, box_bytes);
         for (int idx = i0; idx < i0 + n && ok; ++idx) {
           const KeyTile kt = key_tile(*px, idx);
 #pragma unroll 1
@@ -1084,8 +1066,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               push(full);
             } else {
               const uint32_t ex = h ? ex1 : ex0;
-              fetch(idx + 1, h);
-              ok = convert(2 + h, 128, item, lw * 4 + sub8, 8, piece8, sub8, 4, ex);
+              const bool has_n = fetch(idx + 1, h);
+              ok = rebuild(h, item + 32 * lw * 128, 4, sub4, piece4, 0, ex);
+              if (ok && has_n) copy_raw(&p.map_v, h, slot_n, 0, (int)rank * 128, box_bytes);
+              used += h;
               if (!ok) break;
               signal(full);
             }
@@ -1094,6 +1078,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         flush();
       }
       land(sm.v_full, kNV, uv);
+      land_raw(asked);
     }
     if (bad) record_status(ctl, kStatusArg);
   } else {
@@ -1506,8 +1491,8 @@ cudaError_t launch_paged_tc(const PagedParams& a, float* ws, const DevCtl& ctl, 
   p.spread = {16u, 240u};
   p.use_tma = a.num_pages > 0;
   const bool e4 = a.cache_dtype == kCacheE4M3;
-  if (p.use_tma && (!encode_pool(&p.map_k, a.kp, a, 4, e4 ? 32 : 64, 256) ||
-                    !encode_pool(&p.map_v, a.vp, a, 2, 64, 128)))
+  if (p.use_tma && (!encode_pool(&p.map_k, a.kp, a, 4, e4 ? 16 : 64, 256) ||
+                    !encode_pool(&p.map_v, a.vp, a, 2, e4 ? 32 : 64, 128)))
     return cudaErrorUnknown;
   const int group = group_size(a);
   const long long unit_tiles = (long long)a.Hkv * p.n_tiles;
