@@ -743,7 +743,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // Warps 8 and 9 bring Q and K, warps 10 and 11 V: a warp that waits for its
     // copies to land must not hold back the other operand's.
     const int lw = warp & 1;
-    const Segment* px = nullptr;
+    Segment x;                                // the current segment, in registers
+    x.it0 = x.n = 0;
     bool bad = false;
     // Full barriers (even CTA) of the cp.async items in flight, oldest first.
     uint32_t pend0 = 0, pend1 = 0;
@@ -805,13 +806,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int box = min(1 << p.page_shift, 64);                    // rows per box
     const int boxes = 64 / box;                                    // per 64 keys
     auto peek = [&](int idx, int row, int tma_row) -> int {
-      if (idx >= px->it0 + px->n) return kNoRow;
-      const KeyTile kt = key_tile(*px, idx);
+      if (idx >= x.it0 + x.n) return kNoRow;
+      const KeyTile kt = key_tile(x, idx);
       if (kt.chunk) return kNoRow;
       const int at = kt.tile * kBN;
-      if (kE4M3) return page_seen(p, *px, at + row);
-      const bool tma = p.use_tma && whole_tile(p, *px, kt);
-      return page_of(p, *px, at + (tma ? tma_row : row));
+      if (kE4M3) return page_seen(p, x, at + row);
+      const bool tma = p.use_tma && whole_tile(p, x, kt);
+      return page_of(p, x, at + (tma ? tma_row : row));
     };
     // e4m3.  A warp copies (TMA) and rebuilds rows of its own, 32 of K or of a V half
     // item, in two pieces: a piece's next copy starts as soon as it has been read and
@@ -823,15 +824,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t used = 0;                        // tiles whose pieces have been used up
     // Piece h's copy: its rows, from the slots of lanes l0 and l0 + 16 (V in pages of
     // 16 tokens: two boxes).
-    auto copy_raw = [&](const CUtensorMap* map, int h, int slot, int l0, int x, int bytes) {
+    auto copy_raw = [&](const CUtensorMap* map, int h, int slot, int l0, int col, int bytes) {
       if (!p.use_tma) return;
       const int past = p.num_pages << p.page_shift;
       const int s0 = __shfl_sync(0xffffffffu, slot, l0), s1 = __shfl_sync(0xffffffffu, slot, 16);
       if (lane == 0) {
         mbar_arrive_expect_tx(&raw_full[h], kRawPiece);
-        tma_load_3d_at(raw_u + h * kRawPiece, map, &raw_full[h], x, s0 < 0 ? past : s0, px->g);
+        tma_load_3d_at(raw_u + h * kRawPiece, map, &raw_full[h], col, s0 < 0 ? past : s0, x.g);
         if (bytes < kRawPiece)
-          tma_load_3d_at(raw_u + h * kRawPiece + bytes, map, &raw_full[h], x, s1 < 0 ? past : s1, px->g);
+          tma_load_3d_at(raw_u + h * kRawPiece + bytes, map, &raw_full[h], col, s1 < 0 ? past : s1, x.g);
       }
       __syncwarp();
     };
@@ -912,10 +913,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int page = kNoRow;
       auto copy_k = [&](const KeyTile& kt, uint32_t item) {
         const int at = kt.tile * kBN;
-        const int mine = kt.chunk ? chunk_row(p, *px, codes, at + 64 * (int)rank + row32)
+        const int mine = kt.chunk ? chunk_row(p, x, codes, at + 64 * (int)rank + row32)
                                   : slot_of(p, at + my_row, page, bad);
         const uint8_t* base =
-            static_cast<const uint8_t*>(kt.chunk ? p.k : p.kp) + (px->g * (kD * 2) + lane * 16);
+            static_cast<const uint8_t*>(kt.chunk ? p.k : p.kp) + (x.g * (kD * 2) + lane * 16);
         copy_rows(mine, base, pitch, item + (lane >> 3) * kKBlk, 32, lw, 2, 0, 1);
       };
       // e4m3: this lane's row of the next tile, its slot (-1: no such tile) and exponent.
@@ -924,18 +925,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t ex_n = kNoExp, asked = 0;
       auto fetch = [&](int idx) {
         has_n = false;
-        if (!kE4M3 || idx >= px->it0 + px->n) return;
-        const KeyTile kt = key_tile(*px, idx);
+        if (!kE4M3 || idx >= x.it0 + x.n) return;
+        const KeyTile kt = key_tile(x, idx);
         if (kt.chunk) return;
         const int at = kt.tile * kBN + my_row;
         slot_n = slot_of(p, at, page, bad);
         page = peek(idx + 1, my_row, 0);
-        ex_n = row_exp(p, p.ke, row_seen(p, *px, at) ? slot_n : -1, px->g);
+        ex_n = row_exp(p, p.ke, row_seen(p, x, at) ? slot_n : -1, x.g);
         has_n = true;
         ++asked;
       };
-      while ((px = next_segment()) != nullptr) {
-        const int i0 = px->it0, n = px->n;
+      while (const Segment* px = next_segment()) {
+        x = *px;
+        const int i0 = x.it0, n = x.n;
         if (n == 0) continue;
         page = peek(i0, my_row, tma_row);
         fetch(i0);
@@ -949,29 +951,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!ok) continue;
         {
           const uint8_t* qb = static_cast<const uint8_t*>(p.q) + lane * 16 +
-                              ((long long)px->b * p.Sq * p.Hq + (long long)px->g * p.G) * (kD * 2);
+                              ((long long)x.b * p.Sq * p.Hq + (long long)x.g * p.G) * (kD * 2);
           const uint32_t dst = sQ_u + (lane >> 3) * kQBlk;
 #pragma unroll 4
           for (int it = 0; it < 64; ++it) {
             const int r = it * 2 + lw;
             const int row = (int)rank * kBM + r;
-            const int tok = px->tq0 + (row >> p.g_shift);
-            const int at = min(tok, px->tq1) * p.Hq + (row & (p.G - 1));
+            const int tok = x.tq0 + (row >> p.g_shift);
+            const int at = min(tok, x.tq1) * p.Hq + (row & (p.G - 1));
             cp_async16(dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
-                       qb + (long long)at * (kD * 2), tok <= px->tq1);
+                       qb + (long long)at * (kD * 2), tok <= x.tq1);
           }
           push(bar_full(&sm.q_full));
         }
         for (int idx = i0; idx < i0 + n; ++idx) {
-          const KeyTile kt = key_tile(*px, idx);
+          const KeyTile kt = key_tile(x, idx);
           const int s = (int)(uk % kNK);
           const uint32_t item = kring_u + s * kKItem;
           ok = acquire(&sm.k_empty[s], uk / kNK);
           if (!ok) break;
           ++uk;
           const uint32_t full = bar_full(&sm.k_full[s]);
-          if (!kE4M3 && p.use_tma && whole_tile(p, *px, kt)) {
-            tma_item(&p.map_k, &sm.k_full[s], item, 4 * px->g, 4, kt.tile * kBN + 64 * (int)rank, page);
+          if (!kE4M3 && p.use_tma && whole_tile(p, x, kt)) {
+            tma_item(&p.map_k, &sm.k_full[s], item, 4 * x.g, 4, kt.tile * kBN + 64 * (int)rank, page);
             page = peek(idx + 1, my_row, tma_row);
             if (n_pend > 0) flush();           // Q
           } else if (!kE4M3 || kt.chunk) {
@@ -1006,42 +1008,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int page0 = kNoRow, page1 = kNoRow;
       auto copy_v = [&](const KeyTile& kt, int h, uint32_t item) {
         const int at = kt.tile * kBN + 64 * h;
-        const int mine = kt.chunk ? chunk_row(p, *px, codes, at + row16)
+        const int mine = kt.chunk ? chunk_row(p, x, codes, at + row16)
                                   : slot_of(p, at + my_row, h ? page1 : page0, bad);
         const int ch = lane & 15;
         const uint8_t* base = static_cast<const uint8_t*>(kt.chunk ? p.v : p.vp) +
-                              (px->g * (kD * 2) + (int)rank * 256 + ch * 16);
+                              (x.g * (kD * 2) + (int)rank * 256 + ch * 16);
         copy_rows(mine, base, pitch, item + (ch >> 3) * kKBlk, 16, lw * 2 + (lane >> 4), 4,
                   lane >> 4, 2);
       };
-      // e4m3: this lane's row of the next half item (false: none), its exponent.
-      uint32_t ex0 = kNoExp, ex1 = kNoExp, asked = 0;
-      int slot_n = -1;
-      auto fetch = [&](int idx, int h) -> bool {
-        if (!kE4M3 || idx >= px->it0 + px->n) return false;
-        const KeyTile kt = key_tile(*px, idx);
-        if (kt.chunk) return false;
-        const int at = kt.tile * kBN + 64 * h + my_row;
-        slot_n = slot_of(p, at, h ? page1 : page0, bad);
-        const int next = peek(idx + 1, 64 * h + my_row, 0);
-        const uint32_t e = row_exp(p, p.ve, row_seen(p, *px, at) ? slot_n : -1, px->g);
-        page0 = h ? page0 : next;
-        page1 = h ? next : page1;
-        ex0 = h ? ex0 : e;
-        ex1 = h ? e : ex1;
-        asked += h;
-        return true;
+      // e4m3: this lane's rows (one of each half) of the next tile, their exponents.
+      uint32_t exn0 = kNoExp, exn1 = kNoExp, asked = 0;
+      int slot0 = -1, slot1 = -1;
+      bool has_n = false;
+      auto fetch = [&](int idx) {
+        has_n = false;
+        if (!kE4M3 || idx >= x.it0 + x.n) return;
+        const KeyTile kt = key_tile(x, idx);
+        if (kt.chunk) return;
+        const int at = kt.tile * kBN + my_row;
+        slot0 = slot_of(p, at, page0, bad);
+        slot1 = slot_of(p, at + 64, page1, bad);
+        page0 = peek(idx + 1, my_row, 0);
+        page1 = peek(idx + 1, 64 + my_row, 0);
+        exn0 = row_exp(p, p.ve, row_seen(p, x, at) ? slot0 : -1, x.g);
+        exn1 = row_exp(p, p.ve, row_seen(p, x, at + 64) ? slot1 : -1, x.g);
+        has_n = true;
+        ++asked;
       };
-      while ((px = next_segment()) != nullptr) {
-        const int i0 = px->it0, n = px->n;
+      while (const Segment* px = next_segment()) {
+        x = *px;
+        const int i0 = x.it0, n = x.n;
         if (n == 0) continue;
         page0 = peek(i0, my_row, tma_row);
         page1 = peek(i0, 64 + my_row, 64 + tma_row);
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h)
-          if (fetch(i0, h)) copy_raw(&p.map_v, h, slot_n, 0, (int)rank * 128, box_bytes);
+        fetch(i0);
+        if (has_n) {
+          copy_raw(&p.map_v, 0, slot0, 0, (int)rank * 128, box_bytes);
+          copy_raw(&p.map_v, 1, slot1, 0, (int)rank * 128, box_bytes);
+        }
         for (int idx = i0; idx < i0 + n && ok; ++idx) {
-          const KeyTile kt = key_tile(*px, idx);
+          const KeyTile kt = key_tile(x, idx);
+          const uint32_t ex0 = exn0, ex1 = exn1;
+          if (kE4M3) fetch(idx + 1);
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             const int s = (int)(uv % kNV);
@@ -1051,9 +1059,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ++uv;
             const uint32_t full = bar_full(&sm.v_full[s]);
             if (!kE4M3) {
-              const bool tma = p.use_tma && whole_tile(p, *px, kt);
+              const bool tma = p.use_tma && whole_tile(p, x, kt);
               if (tma)
-                tma_item(&p.map_v, &sm.v_full[s], item, 4 * px->g + 2 * (int)rank, 2,
+                tma_item(&p.map_v, &sm.v_full[s], item, 4 * x.g + 2 * (int)rank, 2,
                          kt.tile * kBN + 64 * h, h ? page1 : page0);
               else
                 copy_v(kt, h, item);
@@ -1065,10 +1073,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               copy_v(kt, h, item);
               push(full);
             } else {
-              const uint32_t ex = h ? ex1 : ex0;
-              const bool has_n = fetch(idx + 1, h);
-              ok = rebuild(h, item + 32 * lw * 128, 4, sub4, piece4, 0, ex);
-              if (ok && has_n) copy_raw(&p.map_v, h, slot_n, 0, (int)rank * 128, box_bytes);
+              ok = rebuild(h, item + 32 * lw * 128, 4, sub4, piece4, 0, h ? ex1 : ex0);
+              if (ok && has_n)
+                copy_raw(&p.map_v, h, h ? slot1 : slot0, 0, (int)rank * 128, box_bytes);
               used += h;
               if (!ok) break;
               signal(full);
