@@ -182,6 +182,7 @@ __device__ __forceinline__ bool in_window(int len, int i, int j, int window, int
 // (paged_tc.cu).  Sequences are scheduled in groups of kPagedTcGroup.
 constexpr int kPagedTcGroup = 64;
 struct PagedTcParams : PagedParams {
+  CUtensorMap map_q, map_o;  // query and output rows
   CUtensorMap map_k, map_v;  // the pools, if use_tma (there is a page)
   int use_tma;
   float* ws;                 // partials [n_clusters * 2][256 rows][256], then (m, l)

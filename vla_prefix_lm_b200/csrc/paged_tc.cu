@@ -906,7 +906,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     const uint32_t pitch = (uint32_t)p.Hkv * (kD * 2);             // bf16 rows
     if (warp < 10) {
-      const uint32_t kring_u = smem_u32(kring), sQ_u = smem_u32(sQ);
+      const uint32_t kring_u = smem_u32(kring);
       const int my_row = 64 * (int)rank + (kE4M3 ? 32 * lw + lane : row32);
       const int tma_row = 64 * (int)rank + (boxes == 1 ? 0 : min(lane >> 2, boxes - 1) * box);
       uint32_t uk = 0, nq = 0;
@@ -945,25 +945,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           copy_raw(&p.map_k, 0, slot_n, 0, 0, kRawPiece);
           copy_raw(&p.map_k, 1, slot_n, 16, 0, kRawPiece);
         }
-        // Q: 32 lanes per row; rows past the unit's last token are zeros.
+        // Q: this CTA's 128 rows in one box; tokens past the chunk are zeros.  (Warp 9
+        // only counts in; nobody waits for Q of a failed run.)
         ok = acquire(&sm.q_empty, nq);
         ++nq;
         if (!ok) continue;
-        {
-          const uint8_t* qb = static_cast<const uint8_t*>(p.q) + lane * 16 +
-                              ((long long)x.b * p.Sq * p.Hq + (long long)x.g * p.G) * (kD * 2);
-          const uint32_t dst = sQ_u + (lane >> 3) * kQBlk;
-#pragma unroll 4
-          for (int it = 0; it < 64; ++it) {
-            const int r = it * 2 + lw;
-            const int row = (int)rank * kBM + r;
-            const int tok = x.tq0 + (row >> p.g_shift);
-            const int at = min(tok, x.tq1) * p.Hq + (row & (p.G - 1));
-            cp_async16(dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
-                       qb + (long long)at * (kD * 2), tok <= x.tq1);
-          }
-          push(bar_full(&sm.q_full));
+        if (leader && lw == 0 && lane == 0) mbar_arrive_expect_tx(&sm.q_full, 2 * kQBytes);
+        __syncwarp();
+        if (lane == 0) {
+          if (lw == 0)
+            tma_load_5d_pair(smem_u32(sQ), &p.map_q, bar_full(&sm.q_full), 0, x.g * p.G,
+                             x.tq0 + (((int)rank * kBM) >> p.g_shift), 0, x.b);
+          if (!(leader && lw == 0)) mbar_arrive_remote(bar_full(&sm.q_full));
         }
+        __syncwarp();
         for (int idx = i0; idx < i0 + n; ++idx) {
           const KeyTile kt = key_tile(x, idx);
           const int s = (int)(uk % kNK);
@@ -975,7 +970,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!kE4M3 && p.use_tma && whole_tile(p, x, kt)) {
             tma_item(&p.map_k, &sm.k_full[s], item, 4 * x.g, 4, kt.tile * kBN + 64 * (int)rank, page);
             page = peek(idx + 1, my_row, tma_row);
-            if (n_pend > 0) flush();           // Q
           } else if (!kE4M3 || kt.chunk) {
             copy_k(kt, item);
             if (!kE4M3) page = peek(idx + 1, my_row, tma_row);
@@ -992,12 +986,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ++used;
             if (!ok) break;
             signal(full);
-            if (n_pend > 0) flush();           // Q
           }
         }
         flush();
       }
       land(sm.k_full, kNK, uk);
+      land(&sm.q_full, 1, nq);
       land_raw(asked);
     } else {
       const uint32_t vring_u = smem_u32(vring);
@@ -1102,6 +1096,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint8_t* const p_row = sP + half * kPBlk + r * 128;   // this thread's line of P
     uint8_t* const st = sP + half * kPBlk + quarter * 4096;   // this warp's 32 lines
     uint32_t gt = 0, n_pair = 0;
+    bool store_pending = false;                    // this warp's output stores may still read P
     // Meets the quarter's other warp; what either wrote before is visible after.
     auto pair_sync = [&]() -> bool {
       __syncwarp();
@@ -1238,6 +1233,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!warp_wait(&sm.o_done, (gt - 1) & 1, sm, ctl)) { ok = false; break; }
           tc_fence_after();
         }
+        if (store_pending) {                       // the last output's stores read P
+          if (lane == 0) tma_store_wait_read();
+          __syncwarp();
+          store_pending = false;
+        }
         const bool rescale = __any_sync(0xffffffffu, need_o);
         if (rescale) {
           const float a = need_o ? alpha : 1.f;
@@ -1269,6 +1269,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_fence_after();
       // The row's other half of l, through the P line (free: the last PV is done).
       float l_all;
+      if (store_pending) {                         // (a segment of one tile before this one)
+        if (lane == 0) tma_store_wait_read();
+        __syncwarp();
+        store_pending = false;
+      }
       {
         float* const mine = reinterpret_cast<float*>(p_row);
         const float* const other = reinterpret_cast<const float*>(sP + (1 - half) * kPBlk + r * 128);
@@ -1279,9 +1284,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (po == nullptr) {
         const float inv = l_all > 0.f ? 1.f / l_all : 0.f;
-        // Each warp stages 32 rows of 64 columns in its own P lines (another
-        // warp may already write the next segment's P), then writes row pieces
-        // of 128 bytes.
+        // Each warp stages 32 rows of 64 columns in its own P lines (another warp may
+        // already write the next segment's P) and stores them as one box; tokens past
+        // the chunk are clipped.
 #pragma unroll 1
         for (int sub = 0; sub < 2; ++sub) {
           uint32_t o0[32], o1[32];
@@ -1290,6 +1295,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
           reg_fence(o0);
           reg_fence(o1);
+          if (sub == 1) {                          // this warp's part of O has been read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive_remote(o_free_l);
+              tma_store_wait_read();               // the first half's lines
+            }
+            __syncwarp();
+          }
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             uint32_t w[4];
@@ -1304,24 +1318,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(st + lane * 128 + ((j ^ (lane & 7)) << 4)) =
                 make_uint4(w[0], w[1], w[2], w[3]);
           }
-          if (sub == 1) {                          // this warp's part of O has been read
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(o_free_l);
-          }
+          fence_proxy_async_smem();
           __syncwarp();
-#pragma unroll
-          for (int it = 0; it < 8; ++it) {
-            const int rr = it * 4 + (lane >> 3), ch = lane & 7;
-            const long long at = __shfl_sync(0xffffffffu, orow, rr);
-            const bool v = __shfl_sync(0xffffffffu, (int)row_valid, rr) != 0;
-            const uint4 w = *reinterpret_cast<const uint4*>(st + rr * 128 + ((ch ^ (rr & 7)) << 4));
-            if (v)
-              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + at * (kD * 2) + half * 256 +
-                                        sub * 128 + ch * 16) = w;
+          const int tok0 = x.tq0 + (((int)rank * kBM + quarter * 32) >> p.g_shift);
+          if (lane == 0 && tok0 <= x.tq1) {
+            tma_store_5d(&p.map_o, st, 0, x.g * p.G, tok0, 2 * half + sub, x.b);
+            tma_store_commit();
           }
           __syncwarp();
         }
+        store_pending = true;
         if (p.lse && row_valid && half == 0)
           p.lse[orow] = l_all > 0.f ? (m_run + __log2f(l_all)) * 0.69314718055994531f
                                     : (l_all == l_all ? -INFINITY : l_all);
@@ -1346,6 +1352,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (row_valid && half == 0) *reinterpret_cast<float2*>(pml) = make_float2(m_run, l_all);
       }
     }
+    if (store_pending && lane == 0) tma_store_wait_read();
+    __syncwarp();
   }
 
   // Neither CTA may leave while its partner can still signal its barriers or
@@ -1451,9 +1459,36 @@ bool encode_pool(CUtensorMap* map, const void* base, const PagedParams& p, uint3
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Whether a group of nb sequences may be cut: with four units or more per
-// cluster the last round's idle clusters cost less than partials and a merge.
-bool may_cut(long long n_units, int slots) { return n_units < 4ll * slots; }
+// Query or output rows [B][Sq][Hq][256] as (64, heads, tokens, 4 column blocks,
+// B): a box of G heads, n / G tokens and `blocks` blocks is n rows of a tile.
+bool encode_rows5(CUtensorMap* map, const void* base, const PagedTcParams& p, uint32_t n,
+                  uint32_t blocks) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t row = 2 * kD;
+  cuuint64_t dims[5] = {64, (cuuint64_t)p.Hq, (cuuint64_t)p.Sq, 4, (cuuint64_t)p.B};
+  cuuint64_t strides[4] = {row, row * p.Hq, 128, row * p.Hq * p.Sq};
+  cuuint32_t box[5] = {64, (cuuint32_t)p.G, n / (uint32_t)p.G, blocks, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whether n_units units may be cut.  Not with four or more per cluster: the last
+// round's idle clusters cost less than partials and a merge.  Nor if the longest
+// cache the page table can hold has few tiles and cutting would not pay for a full
+// batch: then the merge kernel (6 us of 32 at 32 sequences of 816 + 51 tokens) is
+// not launched, and a ragged batch loses at most those few tiles' time.
+bool may_cut(const PagedParams& p, long long n_units, int slots) {
+  if (n_units >= 4ll * slots) return false;
+  const long long nom = (((long long)p.max_pages << p.page_shift) + kBN - 1) / kBN +
+                        (p.Sq + kBN - 1) / kBN;
+  const long long per = (nom * n_units + slots - 1) / slots;
+  const long long rounds = (n_units + slots - 1) / slots;
+  return nom > 16 || rounds * nom > (per > 2 ? per : 2) + 5;
+}
 
 int slots() { return max(sm_count() / 2, 1); }
 
@@ -1481,7 +1516,7 @@ size_t paged_tc_workspace_bytes(const PagedParams& p) {
   // The last group of sequences is the smallest: it decides.
   const int last = p.B % group ? p.B % group : group;
   size_t n = 0;
-  if (may_cut(last * units, slots())) n += (size_t)slots() * 2 * kRowsTile * (kD + 2) * sizeof(float);
+  if (may_cut(p, last * units, slots())) n += (size_t)slots() * 2 * kRowsTile * (kD + 2) * sizeof(float);
   if (p.Sq > kSmemTokens) n += (size_t)slots() * 2 * pad_tokens(p.Sq) * sizeof(uint16_t);
   return n;
 }
@@ -1501,16 +1536,18 @@ cudaError_t launch_paged_tc(const PagedParams& a, float* ws, const DevCtl& ctl, 
   if (p.use_tma && (!encode_pool(&p.map_k, a.kp, a, 4, e4 ? 16 : 64, 256) ||
                     !encode_pool(&p.map_v, a.vp, a, 2, e4 ? 32 : 64, 128)))
     return cudaErrorUnknown;
+  if (!encode_rows5(&p.map_q, a.q, p, kBM, 4) || !encode_rows5(&p.map_o, a.out, p, 32, 1))
+    return cudaErrorUnknown;
   const int group = group_size(a);
   const long long unit_tiles = (long long)a.Hkv * p.n_tiles;
-  const bool any_cut = may_cut((a.B % group ? a.B % group : group) * unit_tiles, slots());
+  const bool any_cut = may_cut(a, (a.B % group ? a.B % group : group) * unit_tiles, slots());
   p.codes = reinterpret_cast<uint16_t*>(
       ws + (any_cut ? (size_t)slots() * 2 * kRowsTile * (kD + 2) : 0));
   for (int b0 = 0; b0 < a.B; b0 += group) {
     p.b0 = b0;
     p.nb = min(group, a.B - b0);
     const long long n_units = (long long)p.nb * a.Hkv * p.n_tiles;
-    p.may_cut = may_cut(n_units, slots()) ? 1 : 0;
+    p.may_cut = any_cut && may_cut(a, n_units, slots()) ? 1 : 0;
     p.n_clusters = p.may_cut ? slots() : (int)min(n_units, (long long)slots());
     const cudaError_t e = e4 ? launch<true>(p, ctl, st) : launch<false>(p, ctl, st);
     if (e != cudaSuccess) return e;
