@@ -5,10 +5,12 @@
 // products, so the kernel spreads the cache over the whole GPU and keeps the
 // arithmetic off the critical path with warp-level tensor instructions.
 //
-//  * Work is cut into 16-key tiles (never across a page) of all sequences and
-//    kv heads in a row; every CTA takes an equal range of them, derived on the
-//    device from cache_lens, so ragged lengths and few long sequences fill the
-//    GPU alike.  A CTA's four warps take its tiles in turn, each through its own
+//  * Work is cut into 16-key tiles (never across a page), shared out on the device
+//    from cache_lens, so that ragged lengths and few long sequences fill the GPU
+//    alike: each sequence's tiles in equal pieces of at most `per`, one CTA a piece,
+//    or, with more sequences than half the CTAs, all tiles in a row in equal
+//    ranges.  (A CTA whose range crosses into another sequence starts over with its
+//    queries: 4 us of 12 at 32 sequences of 880 tokens.)  A CTA's four warps take its tiles in turn, each through its own
 //    16-key stage: one TMA box per tile and operand, K refilled as soon as the
 //    scores are done, V as soon as the product is.
 //  * Scores transposed, S^T = K Q^T by mma.m16n8k16, so that the 8 query rows
@@ -59,9 +61,11 @@ struct Cfg {
 };
 
 struct Plan {
-  int cum[kGroup + 1];                      // tiles before each sequence's units
+  int cum[kGroup + 1];                      // tiles, or pieces, before each sequence's units
   int len[kGroup];
   int part[kWarps];
+  int per;                                  // tiles per CTA
+  bool pieces;                              // units are cut one by one
 };
 struct Smem {
   Plan plan;
@@ -124,8 +128,7 @@ __device__ __forceinline__ uint32_t movm_trans(uint32_t x) {
   return y;
 }
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -147,45 +150,58 @@ __device__ __forceinline__ Seen seen_tiles(const PagedDecodeParams& p, int len) 
   return s;
 }
 
-// Block-wide: tiles before each sequence (its cached tiles and one of the
-// chunk, times the kv heads), from cache_lens.  All kThreads threads call it.
-__device__ void make_plan(const PagedDecodeParams& p, const DevCtl& ctl, Plan& plan) {
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  int carry = 0;
-  bool bad = false;
-  for (int base = 0; base < p.nb; base += kThreads) {
-    const int b = base + t;
-    int x = 0;
-    if (b < p.nb) {
-      const int n = cached_len(p.lens, p.b0 + b, p.max_pages, p.page_shift, bad);
-      plan.len[b] = n;
-      x = (seen_tiles(p, n).count + 1) * p.Hkv;
-    }
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, off);
-      if (lane >= off) x += y;
-    }
-    if (lane == 31) plan.part[warp] = x;
-    __syncthreads();
-    int before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      before += w < warp ? plan.part[w] : 0;
-      total += plan.part[w];
-    }
-    if (b < p.nb) plan.cum[b + 1] = carry + before + x;
-    carry += total;
-    __syncthreads();
-  }
-  if (t == 0) plan.cum[0] = 0;
-  if (bad && blockIdx.x == 0) record_status(ctl, kStatusArg);
-  __syncthreads();
+// Tiles of a unit: its cached ones and one of the chunk's own keys.
+__device__ __forceinline__ int unit_tiles_of(const PagedDecodeParams& p, int len) {
+  return seen_tiles(p, len).count + 1;
 }
 
-// Tiles per CTA: equal ranges, at least one tile per warp.
-__device__ __forceinline__ int tiles_per_cta(const PagedDecodeParams& p, const Plan& plan) {
-  return max((plan.cum[p.nb] + p.n_ctas - 1) / p.n_ctas, kWarps);
+// Block-wide: the plan, from cache_lens.  All kThreads threads call it.
+__device__ void make_plan(const PagedDecodeParams& p, const DevCtl& ctl, Plan& plan) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  // cum[b + 1] = sum of count(length) over sequences 0 .. b, times the kv heads;
+  // returns the total.
+  auto scan = [&](auto count) -> int {
+    int carry = 0;
+    for (int base = 0; base < p.nb; base += kThreads) {
+      const int b = base + t;
+      int x = b < p.nb ? count(plan.len[b]) * p.Hkv : 0;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+      }
+      if (lane == 31) plan.part[warp] = x;
+      __syncthreads();
+      int before = 0, total = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        before += w < warp ? plan.part[w] : 0;
+        total += plan.part[w];
+      }
+      if (b < p.nb) plan.cum[b + 1] = carry + before + x;
+      carry += total;
+      __syncthreads();
+    }
+    return carry;
+  };
+  bool bad = false;
+  for (int b = t; b < p.nb; b += kThreads)
+    plan.len[b] = cached_len(p.lens, p.b0 + b, p.max_pages, p.page_shift, bad);
+  if (bad && blockIdx.x == 0) record_status(ctl, kStatusArg);
+  __syncthreads();
+  const int total = scan([&](int n) { return unit_tiles_of(p, n); });
+  const int units = p.nb * p.Hkv;
+  const bool pieces = 2 * units <= p.n_ctas;
+  // One CTA more per unit than an even share needs: the pieces always fit.
+  const int ctas = pieces ? p.n_ctas - units : p.n_ctas;
+  const int per = max((total + ctas - 1) / ctas, kWarps);
+  if (pieces) (void)scan([&](int n) { return (unit_tiles_of(p, n) + per - 1) / per; });
+  if (t == 0) {
+    plan.cum[0] = 0;
+    plan.per = per;
+    plan.pieces = pieces;
+  }
+  __syncthreads();
 }
 
 __device__ __forceinline__ int find_seq(const Plan& plan, int nb, int pos) {
@@ -227,10 +243,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
   pdl_wait();
   pdl_launch_dependents();
   make_plan(p, ctl, sm.plan);
-  const int per = tiles_per_cta(p, sm.plan);
-  const int total = sm.plan.cum[p.nb];
-  int pos = (int)min((long long)blockIdx.x * per, (long long)total);
-  const int end = min(pos + per, total);
+  const int per = sm.plan.per, total = sm.plan.cum[p.nb];
+  const bool pieces = sm.plan.pieces;
+  const int cta = (int)blockIdx.x;
+  // Tiles [pos, end) of all, or this CTA's piece.
+  int pos = pieces ? cta : (int)min((long long)cta * per, (long long)total);
+  const int end = pieces ? min(cta + 1, total) : min(pos + per, total);
   const int R = p.Sq * p.G;
   const float sl2 = p.scale_log2;
   const uint32_t kt = smem_u32(ring + warp * 2 * C::kBytes), vt = kt + C::kBytes;
@@ -244,10 +262,19 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     const Seen sn = seen_tiles(p, len);
     const int unit_tiles = sn.count + 1;
     const int rem = pos - sm.plan.cum[b];
-    const int h = rem / unit_tiles;
-    const int i0 = rem - h * unit_tiles;
-    const int i1 = min(unit_tiles, i0 + (end - pos));
-    pos += i1 - i0;
+    int h, i0, i1;
+    if (pieces) {
+      const int n = (unit_tiles + per - 1) / per;
+      h = rem / n;
+      i0 = (int)((long long)(rem - h * n) * unit_tiles / n);
+      i1 = (int)((long long)(rem - h * n + 1) * unit_tiles / n);
+      ++pos;
+    } else {
+      h = rem / unit_tiles;
+      i0 = rem - h * unit_tiles;
+      i1 = min(unit_tiles, i0 + (end - pos));
+      pos += i1 - i0;
+    }
     const int bb = p.b0 + b;
     const int32_t* table = p.table + (long long)bb * p.max_pages;
 
@@ -300,6 +327,21 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
       return static_cast<const __nv_bfloat16*>(p.q) + q0 +
              ((long long)(r >> p.g_shift) * p.Hq + (r & (p.G - 1))) * kD;
     };
+    // The chunk's own keys fall to the CTA that has the unit's last tile: warp w has
+    // rows w and w + 4, a lane 8 columns.  Their loads go out now.
+    const bool chunk = i1 == unit_tiles;
+    const int rw[2] = {min(warp, R - 1), min(warp + kWarps, R - 1)};
+    const __nv_bfloat16* kn = static_cast<const __nv_bfloat16*>(p.k);
+    const __nv_bfloat16* vn = static_cast<const __nv_bfloat16*>(p.v);
+    const long long n0 = ((long long)bb * p.Sq * p.Hkv + h) * kD + lane * 8;
+    const long long n_step = (long long)p.Hkv * kD;
+    uint4 cq[2], ck, cv;
+    if (chunk) {
+      cq[0] = *reinterpret_cast<const uint4*>(q_row(rw[0]) + lane * 8);
+      cq[1] = *reinterpret_cast<const uint4*>(q_row(rw[1]) + lane * 8);
+      ck = *reinterpret_cast<const uint4*>(kn + n0);
+      cv = *reinterpret_cast<const uint4*>(vn + n0);
+    }
     // Q^T as the B operand, straight from global memory: bf16: lane (g, t4)
     // holds Q[g][16 kk + 2 t4 ..] and Q[g][16 kk + 8 + 2 t4 ..]; e4m3: Q[g][16 kk
     // + 4 t4 ..] and the two after, as fp16 times a power of two.
@@ -344,41 +386,53 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
         qf1 *= __shfl_sync(0xffffffffu, down, 8 * t4 + 4);
       }
     }
-    // The chunk's own keys, by the CTA that has the unit's last tile: warp w has
-    // rows w and w + 4, a lane 8 columns.
-    const bool chunk = i1 == unit_tiles;
     if (chunk) {
+      float acc[2][8], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[u][c] = 0.f;
 #pragma unroll 1
-      for (int r = warp; r < R; r += kWarps) {
-        const int tq = r >> p.g_shift;
-        const uint32_t cq = __shfl_sync(0xffffffffu, code, tq);
-        float q[8], acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-        load8(q_row(r) + lane * 8, q);
-#pragma unroll 1
-        for (int j = 0; j < p.Sq; ++j) {
-          const uint32_t ck = __shfl_sync(0xffffffffu, code, j);
-          if (!visible(cq, ck) || !in_window(len, tq, j, p.window, p.sinks)) continue;
-          const long long at = (((long long)bb * p.Sq + j) * p.Hkv + h) * kD + lane * 8;
-          float k[8], v[8], sc = 0.f;
-          load8(static_cast<const __nv_bfloat16*>(p.k) + at, k);
-          load8(static_cast<const __nv_bfloat16*>(p.v) + at, v);
+      for (int j = 0; j < p.Sq; ++j) {
+        float k[8], v[8];
+        unpack8(ck, k);
+        unpack8(cv, v);
+        if (j + 1 < p.Sq) {
+          ck = *reinterpret_cast<const uint4*>(kn + n0 + (j + 1) * n_step);
+          cv = *reinterpret_cast<const uint4*>(vn + n0 + (j + 1) * n_step);
+        }
+        const uint32_t code_j = __shfl_sync(0xffffffffu, code, j);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int tq = rw[u] >> p.g_shift;
+          const uint32_t code_q = __shfl_sync(0xffffffffu, code, tq);
+          if (!visible(code_q, code_j) || !in_window(len, tq, j, p.window, p.sinks)) continue;
+          float q[8], sc = 0.f;
+          unpack8(cq[u], q);
 #pragma unroll
           for (int c = 0; c < 8; ++c) sc = fmaf(q[c], k[c], sc);
 #pragma unroll
           for (int sh = 16; sh >= 1; sh >>= 1) sc += __shfl_xor_sync(0xffffffffu, sc, sh);
           sc *= sl2;
-          const float mn = fmaxf(m, sc), f = m == -INFINITY ? 0.f : ex2(m - mn), w = ex2(sc - mn);
-          l = l * f + w;
+          const float mn = fmaxf(m[u], sc), f = m[u] == -INFINITY ? 0.f : ex2(m[u] - mn);
+          const float w = ex2(sc - mn);
+          l[u] = l[u] * f + w;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) acc[c] = fmaf(acc[c], f, w * v[c]);
-          m = mn;
+          for (int c = 0; c < 8; ++c) acc[u][c] = fmaf(acc[u][c], f, w * v[c]);
+          m[u] = mn;
         }
-        float4* dst = reinterpret_cast<float4*>(&sm.o_chunk[r][lane * 8]);
-        dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-        if (lane == 0) {
-          sm.m[kWarps][r] = m;
-          sm.l[kWarps][r] = l;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int r = warp + u * kWarps;
+        if (r < R) {
+          float4* dst = reinterpret_cast<float4*>(&sm.o_chunk[r][lane * 8]);
+          dst[0] = make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]);
+          dst[1] = make_float4(acc[u][4], acc[u][5], acc[u][6], acc[u][7]);
+          if (lane == 0) {
+            sm.m[kWarps][r] = m[u];
+            sm.l[kWarps][r] = l[u];
+          }
         }
       }
     }
@@ -628,8 +682,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
           if (p.lse && c0 == 0)
             p.lse[row] = L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : (L == L ? -INFINITY : L);
         } else {
-          // A range that begins mid-unit is its CTA's first: slot 0, else slot 1.
-          const long long at = ((long long)blockIdx.x * 2 + (i0 > 0 ? 0 : 1)) * kRows + r;
+          // A piece: slot 0.  A range that begins mid-unit is its CTA's first: slot 0,
+          // else slot 1.
+          const long long at = ((long long)cta * 2 + (pieces || i0 > 0 ? 0 : 1)) * kRows + r;
           float* dst = p.ws + at * kD + c0;
 #pragma unroll
           for (int k = 0; k < 4; ++k) *reinterpret_cast<float4*>(dst + 64 * k) = acc[k];
@@ -652,8 +707,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
 
 // Merges the partials of the units that several CTAs read: CTA (unit, row), two
 // groups of 64 threads (4 columns each) that share out the pieces; a thread has
-// four pieces' loads in flight.
-constexpr int kMergeFlight = 4;
+// eight pieces' loads in flight.
+constexpr int kMergeFlight = 8;
 __global__ void __launch_bounds__(kThreads)
     paged_decode_merge(const __grid_constant__ PagedDecodeParams p, const DevCtl ctl) {
   __shared__ Plan plan;
@@ -662,33 +717,38 @@ __global__ void __launch_bounds__(kThreads)
   pdl_wait();                  // the partials come from the kernel before
   pdl_launch_dependents();
   make_plan(p, ctl, plan);
-  const int per = tiles_per_cta(p, plan);
+  const int per = plan.per;
   const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
-  const int tiles = (plan.cum[b + 1] - plan.cum[b]) / p.Hkv;
-  const int t0 = plan.cum[b] + h * tiles;
-  const int c0 = t0 / per, c1 = (t0 + tiles - 1) / per;
+  const int n = (plan.cum[b + 1] - plan.cum[b]) / p.Hkv;    // the unit's pieces or tiles
+  const int t0 = plan.cum[b] + h * n;
+  const int c0 = plan.pieces ? t0 : t0 / per, c1 = plan.pieces ? t0 + n - 1 : (t0 + n - 1) / per;
   if (c0 == c1) return;        // read whole
+  const int first = plan.pieces ? 0 : 1;       // slot of the unit's first range
   const int r = blockIdx.y;
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 6, col = (threadIdx.x & 63) * 4;
   const float2* ml = reinterpret_cast<const float2*>(p.ws + (long long)p.n_ctas * 2 * kRows * kD);
-  auto slot = [&](int c) { return ((long long)c * 2 + (c == c0 ? 1 : 0)) * kRows + r; };
-  float M = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) {
-    const float2 v = ml[slot(c)];
-    if (v.y > 0.f) M = fmaxf(M, v.x);
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  float acc[4] = {0.f, 0.f, 0.f, 0.f}, L = 0.f;
-  for (int cb = c0 + grp; cb <= c1; cb += 2 * kMergeFlight) {
-    float2 v[kMergeFlight];
-    float4 x[kMergeFlight];
+  auto slot = [&](int c) { return ((long long)c * 2 + (c == c0 ? first : 0)) * kRows + r; };
+  float2 v[kMergeFlight];
+  float4 x[kMergeFlight];
+  auto fetch = [&](int cb) {
 #pragma unroll
     for (int i = 0; i < kMergeFlight; ++i) {
       const int c = min(cb + 2 * i, c1);
       v[i] = ml[slot(c)];
       x[i] = *reinterpret_cast<const float4*>(p.ws + slot(c) * kD + col);
     }
+  };
+  fetch(c0 + grp);             // under way while the maximum is found
+  float M = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) {
+    const float2 w = ml[slot(c)];
+    if (w.y > 0.f) M = fmaxf(M, w.x);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  float acc[4] = {0.f, 0.f, 0.f, 0.f}, L = 0.f;
+  for (int cb = c0 + grp; cb <= c1; cb += 2 * kMergeFlight) {
+    if (cb != c0 + grp) fetch(cb);
 #pragma unroll
     for (int i = 0; i < kMergeFlight; ++i) {
       // none left, or no visible key (O may hold 0 * inf); NaN goes on
