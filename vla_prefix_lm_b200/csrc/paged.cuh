@@ -106,6 +106,8 @@ struct CacheParams {
   uint8_t* valid_out;                // read: [B, S], may be null
   int B, S, Hkv, d;
   int page_shift, num_pages, max_pages;
+  bool seen_only;                    // read: only rows that a chunk sees (window, sinks)
+  int window, sinks;
 };
 cudaError_t launch_cache(const CacheParams& p, bool write, bool f32, int cache_dtype,
                          const DevCtl& ctl, cudaStream_t st);
@@ -132,6 +134,7 @@ struct PagedParams {
   int cache_dtype;
   bool f32;                          // q, k, v, out
   float scale;
+  bool in_order;                     // bf16 pages [B * max_pages] in order, no table
 };
 
 // A sequence's cached length, clamped to what its page-table row can hold.

@@ -21,7 +21,8 @@
 //     a cycle, about 5700 cycles a tile.)
 //   e4m3: raw rows by TMA into a staging half ahead of their use, then rebuilt as
 //     bf16 by the loader warps, exactly, as the scale is a power of two: no
-//     rounding beside the cache's own.
+//     rounding beside the cache's own.  Chunks of four query tiles and more read
+//     rows that cache.cu rebuilt once into the workspace (expanded_bytes).
 //
 // Work.  Unit = (sequence, kv head, query tile).  Lengths differ by sequence
 // and live on the device, so each cluster derives the schedule itself from
@@ -458,6 +459,7 @@ __device__ __forceinline__ void cp_wait() {
 constexpr int kNoRow = -2147483647 - 1;
 __device__ __forceinline__ int page_of(const PagedTcParams& p, const Segment& s, int x) {
   if (x >= s.len || (p.window > 0 && x < s.lo0 && x >= p.sinks)) return kNoRow;
+  if (p.in_order) return s.b * p.max_pages + (x >> p.page_shift);
   return p.table[(long long)s.b * p.max_pages + (x >> p.page_shift)];
 }
 // Whether some query of the segment sees cached position x.
@@ -1370,9 +1372,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // Merges the partials of units that were cut: out = sum_k 2^(m_k - M) O_k /
 // sum_k 2^(m_k - M) l_k with M the largest m_k that has l_k > 0.  CTA (u, y):
-// rows [32 y, 32 y + 32) of unit u, one warp per row at a time, 8 columns per
-// lane.  HBM-bound: reads the fp32 partials once.
-__global__ void __launch_bounds__(256)
+// every gridDim.y-th eight rows of unit u, a warp each: a lane weighs one partial,
+// then takes 8 columns of all of them, four partials in flight.  Bound by that
+// latency: the partials lie in L2.
+constexpr int kCombineRows = 8;
+__global__ void __launch_bounds__(32 * kCombineRows)
     paged_combine_kernel(const __grid_constant__ PagedTcParams p, const DevCtl ctl) {
   __shared__ Plan plan;
   pdl_wait();                  // the partials come from the kernel before
@@ -1391,32 +1395,62 @@ __global__ void __launch_bounds__(256)
   const int lane = threadIdx.x & 31;
   const float2* ml = reinterpret_cast<const float2*>(
       p.ws + (long long)p.n_clusters * 2 * kRowsTile * kD);
-  for (int i = threadIdx.x >> 5; i < 32; i += 8) {
-    const int row = blockIdx.y * 32 + i;
+  for (int row = blockIdx.y * kCombineRows + (threadIdx.x >> 5); row < p.G * p.tok_per_tile;
+       row += gridDim.y * kCombineRows) {
     const int tok = tile * p.tok_per_tile + (row >> p.g_shift);
-    if (tok >= p.Sq || row >= p.G * p.tok_per_tile) continue;
+    if (tok >= p.Sq) break;
+    // the unit's part of cluster c: its last run in c0, else its first
+    auto at = [&](int c) { return (long long)(c * 2 + (c == c0 ? 1 : 0)) * kRowsTile + row; };
     float M = -INFINITY;
-    for (int c = c0; c <= c1; ++c) {
-      const float2 v = ml[(long long)(c * 2 + (c == c0 ? 1 : 0)) * kRowsTile + row];
+    for (int c = c0 + lane; c <= c1; c += 32) {
+      const float2 v = ml[at(c)];
       if (v.y > 0.f) M = fmaxf(M, v.x);
     }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     float l = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-      const long long at = (long long)(c * 2 + (c == c0 ? 1 : 0)) * kRowsTile + row;
-      const float2 v = ml[at];
-      if (!(v.y > 0.f)) {
-        if (v.y == v.y) continue;            // no visible key; NaN goes on
+    for (int cb = c0; cb <= c1; cb += 32) {
+      const int n = min(c1 - cb + 1, 32);
+      float w = 0.f;
+      bool live = false;         // false: the part saw no key (a NaN goes on)
+      if (lane < n) {
+        const float2 v = ml[at(cb + lane)];
+        live = !(v.y == 0.f);
+        w = live ? ex2(v.x - M) : 0.f;
+        if (live) l += w * v.y;
       }
-      const float w = ex2(v.x - M);
-      l += w * v.y;
-      const float4* src = reinterpret_cast<const float4*>(p.ws + at * kD + lane * 8);
-      const float4 a = src[0], d = src[1];
-      acc[0] += w * a.x; acc[1] += w * a.y; acc[2] += w * a.z; acc[3] += w * a.w;
-      acc[4] += w * d.x; acc[5] += w * d.y; acc[6] += w * d.z; acc[7] += w * d.w;
+      const uint32_t on = __ballot_sync(0xffffffffu, live);
+      for (int j0 = 0; j0 < n; j0 += 4) {
+        float4 a[4], d[4];
+        float wj[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = j0 + j;
+          wj[j] = __shfl_sync(0xffffffffu, w, c & 31);
+          a[j] = d[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (c < n && ((on >> c) & 1u)) {
+            const float4* src = reinterpret_cast<const float4*>(p.ws + at(cb + c) * kD + lane * 8);
+            a[j] = src[0];
+            d[j] = src[1];
+          } else {
+            wj[j] = 0.f;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[0] += wj[j] * a[j].x; acc[1] += wj[j] * a[j].y;
+          acc[2] += wj[j] * a[j].z; acc[3] += wj[j] * a[j].w;
+          acc[4] += wj[j] * d[j].x; acc[5] += wj[j] * d[j].y;
+          acc[6] += wj[j] * d[j].z; acc[7] += wj[j] * d[j].w;
+        }
+      }
     }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
     const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-    const long long orow = ((long long)(p.b0 + b) * p.Sq + tok) * p.Hq + (long long)g * p.G + (row & (p.G - 1));
+    const long long orow =
+        ((long long)(p.b0 + b) * p.Sq + tok) * p.Hq + (long long)g * p.G + (row & (p.G - 1));
     uint4 w;
     w.x = cvt_bf16x2(acc[0] * inv, acc[1] * inv);
     w.y = cvt_bf16x2(acc[2] * inv, acc[3] * inv);
@@ -1510,6 +1544,22 @@ bool paged_tc_applies(const PagedParams& p) {
          (long long)p.B * p.Sq < (1ll << 31) && group_size(p) >= 1;
 }
 
+// e4m3 pages and a chunk of several query tiles: each tile's cluster would rebuild
+// the same rows.  From four tiles on, one pass writes the cached rows that the chunk
+// sees as bf16 into the workspace and the bf16 form reads those.  Measured, rebuilt
+// in every cluster / expanded first, 32 new tokens a tile: four sequences of 15000
+// tokens, 2 tiles 71 / 77 us, 3 tiles 86 / 87, 4 tiles 103 / 98, 8 tiles 178 / 147,
+// 16 tiles 337 / 247; 32 sequences of 816 tokens, 2 tiles 33 / 36, 4 tiles 57 / 54, 8
+// tiles 115 / 103; one of 2000 tokens, 4 tiles 35 / 37.  Not for page tables that
+// reach over more than half a GiB of rows.
+static size_t expanded_bytes(const PagedParams& p) {
+  const int tiles = (p.Sq * (p.Hq / p.Hkv) + kRowsTile - 1) / kRowsTile;
+  if (p.cache_dtype != kCacheE4M3 || tiles < 4 || p.num_pages == 0) return 0;
+  const unsigned long long n =
+      ((unsigned long long)p.max_pages << p.page_shift) * p.B * p.Hkv * (kD * 2);
+  return n <= (1ull << 28) ? (size_t)n : 0;
+}
+
 size_t paged_tc_workspace_bytes(const PagedParams& p) {
   const int G = p.Hq / p.Hkv, group = group_size(p);
   const long long units = (long long)p.Hkv * ((p.Sq + kRowsTile / G - 1) / (kRowsTile / G));
@@ -1518,10 +1568,31 @@ size_t paged_tc_workspace_bytes(const PagedParams& p) {
   size_t n = 0;
   if (may_cut(p, last * units, slots())) n += (size_t)slots() * 2 * kRowsTile * (kD + 2) * sizeof(float);
   if (p.Sq > kSmemTokens) n += (size_t)slots() * 2 * pad_tokens(p.Sq) * sizeof(uint16_t);
-  return n;
+  return n + 2 * expanded_bytes(p);
 }
 
-cudaError_t launch_paged_tc(const PagedParams& a, float* ws, const DevCtl& ctl, cudaStream_t st) {
+cudaError_t launch_paged_tc(const PagedParams& given, float* ws, const DevCtl& ctl,
+                            cudaStream_t st) {
+  PagedParams a = given;
+  if (const size_t n = expanded_bytes(a)) {
+    CacheParams c{};
+    uint8_t* rows = reinterpret_cast<uint8_t*>(ws);
+    ws = reinterpret_cast<float*>(rows + 2 * n);
+    c.k_out = rows; c.v_out = rows + n;
+    c.kp = const_cast<void*>(a.kp); c.vp = const_cast<void*>(a.vp);
+    c.ke = const_cast<uint8_t*>(a.ke); c.ve = const_cast<uint8_t*>(a.ve);
+    c.table = a.table; c.lens = a.lens;
+    c.B = a.B; c.S = a.max_pages << a.page_shift; c.Hkv = a.Hkv; c.d = a.d;
+    c.page_shift = a.page_shift; c.num_pages = a.num_pages; c.max_pages = a.max_pages;
+    c.seen_only = true; c.window = a.window; c.sinks = a.sinks;
+    const cudaError_t e = launch_cache(c, false, false, kCacheE4M3, ctl, st);
+    if (e != cudaSuccess) return e;
+    a.kp = c.k_out; a.vp = c.v_out;
+    a.ke = a.ve = nullptr;
+    a.num_pages = a.B * a.max_pages;
+    a.cache_dtype = kCacheBF16;
+    a.in_order = true;
+  }
   PagedTcParams p{};
   static_cast<PagedParams&>(p) = a;
   p.ws = ws;
@@ -1552,8 +1623,12 @@ cudaError_t launch_paged_tc(const PagedParams& a, float* ws, const DevCtl& ctl, 
     const cudaError_t e = e4 ? launch<true>(p, ctl, st) : launch<false>(p, ctl, st);
     if (e != cudaSuccess) return e;
     if (p.may_cut) {
-      const dim3 grid((unsigned)n_units, kRowsTile / 32);
-      const cudaError_t c = launch_pdl(paged_combine_kernel, grid, dim3(256), 0, st, p, ctl);
+      // A round of CTAs at most: each derives the schedule, cut unit or not.
+      int y = kRowsTile / kCombineRows;
+      while (y > 4 && n_units * y > 4ll * sm_count()) y >>= 1;
+      const dim3 grid((unsigned)n_units, (unsigned)y);
+      const cudaError_t c =
+          launch_pdl(paged_combine_kernel, grid, dim3(32 * kCombineRows), 0, st, p, ctl);
       if (c != cudaSuccess) return c;
     }
   }
