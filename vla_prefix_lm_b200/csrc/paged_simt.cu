@@ -9,6 +9,11 @@
 // per four keys; four consecutive cached positions never cross a page.
 // Masked keys are never loaded, so nothing they hold (NaN in a stale slot)
 // reaches the result.
+//
+// Bound by that chain of dependent steps.  So the eight warps of a CTA share one row,
+// every eighth group of four keys each, and merge their states through shared
+// memory; only many rows of few keys are left whole to a warp each, which saves that
+// merge (split_rows).
 #include <cfloat>
 
 #include "launch.h"
@@ -19,7 +24,8 @@ namespace piattn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 4;                   // new tokens per CTA
+constexpr int kWarps = kThreads / 32;
+constexpr int kTokens = 4;                   // new tokens per CTA (whole rows per warp)
 
 template <int C>
 __device__ __forceinline__ void load_row(const float* p, float (&x)[C]) {
@@ -106,11 +112,15 @@ struct Row {
   }
 };
 
-template <int D, typename T, typename TC>
+// kSplit: a CTA's warps share one row (blockIdx.x), else each takes rows of its own
+// among the CTA's kTokens tokens.
+template <int D, typename T, typename TC, bool kSplit>
 __global__ void __launch_bounds__(kThreads)
     paged_simt_kernel(const __grid_constant__ PagedParams p, const DevCtl ctl) {
   extern __shared__ uint32_t s_codes[];      // [Sq] codes of the new tokens
   __shared__ int s_scan[33];
+  __shared__ float s_acc[kSplit ? kWarps : 1][kSplit ? D : 1];
+  __shared__ float2 s_ml[kWarps];
   constexpr int C = D / 32;
   const int b = blockIdx.y;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -121,8 +131,6 @@ __global__ void __launch_bounds__(kThreads)
   bool bad = false;
   const int len = cached_len(p.lens, b, p.max_pages, p.page_shift, bad);
   const int32_t* table = p.table + (long long)b * p.max_pages;
-  const int tok0 = blockIdx.x * kTokens;
-  const int ntok = min(kTokens, p.Sq - tok0);
   const int group = p.Hq / p.Hkv;
   const int e0 = lane * C;
   const T* kn = static_cast<const T*>(p.k);
@@ -130,9 +138,12 @@ __global__ void __launch_bounds__(kThreads)
   const TC* kp = static_cast<const TC*>(p.kp);
   const TC* vp = static_cast<const TC*>(p.vp);
 
-  for (int r = warp; r < ntok * p.Hq; r += kThreads / 32) {
-    const int i = tok0 + r / p.Hq, h = r % p.Hq, g = h / group;
-    const long long row = ((long long)b * p.Sq + i) * p.Hq + h;
+  const int r_first = kSplit ? blockIdx.x : blockIdx.x * kTokens * p.Hq + warp;
+  const int r_end = kSplit ? blockIdx.x + 1 : min((int)(blockIdx.x + 1) * kTokens, p.Sq) * p.Hq;
+  const int part = kSplit ? warp : 0, parts = kSplit ? kWarps : 1;
+  for (int r = r_first; r < r_end; r += kWarps) {
+    const int i = r / p.Hq, h = r % p.Hq, g = h / group;
+    const long long row = (long long)b * p.Sq * p.Hq + r;
     Row<C> x;
     load_row<C>(static_cast<const T*>(p.q) + row * D + e0, x.q);
 #pragma unroll
@@ -142,14 +153,14 @@ __global__ void __launch_bounds__(kThreads)
     }
     const uint32_t cq = s_codes[i];
     if (!is_pad(cq)) {
+      // Groups of four cached positions: those with sinks, then from the window on.
       const CachedRange cr = cached_range(len, i, p.window, p.sinks);
-      for (int j0 = 0; j0 < len; j0 += 4) {
-        // From the last sink on, continue at the window.
-        if (j0 >= cr.sink_end && j0 + 4 <= cr.lo) j0 = cr.lo & ~3;
-        if (j0 >= len) break;
+      const int n_sink = (cr.sink_end + 3) >> 2, from = max(cr.lo >> 2, n_sink);
+      const int n_groups = n_sink + max(((len + 3) >> 2) - from, 0);
+      for (int gi = part; gi < n_groups; gi += parts) {
+        const int j0 = (gi < n_sink ? gi : from + gi - n_sink) * 4;
         const int page = table[j0 >> p.page_shift];
         const bool ok = page >= 0 && page < p.num_pages;
-        bad = bad || !ok;
         float s[4], v[4][C];
         bool on[4];
 #pragma unroll
@@ -159,6 +170,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
           for (int c = 0; c < C; ++c) v[u][c] = 0.f;
           on[u] = j < len && (j < cr.sink_end || j >= cr.lo);
+          bad = bad || (on[u] && !ok);
           if (on[u] && ok) {
             const long long slot = ((long long)page << p.page_shift) + (j & ((1 << p.page_shift) - 1));
             const long long at = slot * p.Hkv + g;
@@ -177,7 +189,7 @@ __global__ void __launch_bounds__(kThreads)
         }
         x.add4(s, on, v);
       }
-      for (int j0 = 0; j0 < p.Sq; j0 += 4) {
+      for (int j0 = 4 * part; j0 < p.Sq; j0 += 4 * parts) {
         float s[4], v[4][C];
         bool on[4];
 #pragma unroll
@@ -203,26 +215,62 @@ __global__ void __launch_bounds__(kThreads)
         x.add4(s, on, v);
       }
     }
+    if constexpr (kSplit) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) s_acc[warp][e0 + c] = x.acc[c];
+      if (lane == 0) s_ml[warp] = make_float2(x.m, x.l);
+      __syncthreads();
+      if (warp > 0) break;
+      float m = -FLT_MAX;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ml[w].x);   // (-FLT_MAX: saw no key)
+      x.l = 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) x.acc[c] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = expf(s_ml[w].x - m);
+        x.l += f * s_ml[w].y;
+#pragma unroll
+        for (int c = 0; c < C; ++c) x.acc[c] = fmaf(f, s_acc[w][e0 + c], x.acc[c]);
+      }
+      x.m = m;
+    }
     const float inv = x.l > 0.f ? 1.f / x.l : 0.f;   // no visible key (padding): 0
 #pragma unroll
     for (int c = 0; c < C; ++c) x.acc[c] *= inv;
     store_row<C>(static_cast<T*>(p.out) + row * D + e0, x.acc);
-    if (p.lse && lane == 0) p.lse[row] = x.l > 0.f ? x.m + logf(x.l) : -INFINITY;
+    if (p.lse && lane == 0)
+      p.lse[row] = x.l > 0.f ? x.m + logf(x.l) : (x.l == x.l ? -INFINITY : x.l);
   }
   if (bad) record_status(ctl, kStatusArg);
 }
 
-template <int D, typename T, typename TC>
-cudaError_t launch(const PagedParams& p, const DevCtl& ctl, cudaStream_t st) {
+template <int D, typename T, typename TC, bool kSplit>
+cudaError_t launch_as(const PagedParams& p, const DevCtl& ctl, cudaStream_t st) {
   const size_t smem = sizeof(uint32_t) * (size_t)p.Sq;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<D, T, TC>,
+  if (smem > 32 * 1024) {                    // (what else the kernel has is under 16 KB)
+    const cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<D, T, TC, kSplit>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)smem);
     if (e != cudaSuccess) return e;
   }
-  dim3 grid((unsigned)((p.Sq + kTokens - 1) / kTokens), (unsigned)p.B);
-  return launch_pdl(paged_simt_kernel<D, T, TC>, grid, dim3(kThreads), smem, st, p, ctl);
+  const int n = kSplit ? p.Sq * p.Hq : (p.Sq + kTokens - 1) / kTokens;
+  return launch_pdl(paged_simt_kernel<D, T, TC, kSplit>, dim3((unsigned)n, (unsigned)p.B),
+                    dim3(kThreads), smem, st, p, ctl);
+}
+// Measured (fp32, d = 64, 4 heads), rows whole / split: 36 rows of 49 keys 27 / 5.6 us,
+// of 809 keys 495 / 33; 4096 rows of 816 keys 618 / 358; 32768 rows of 864 keys 3011
+// / 2462; 4096 rows of 56 keys 36 / 42; 32768 of 56 keys 181 / 343; 8192 of 104 keys 97
+// / 103, 32768 of 612 keys 1831 / 1746.
+bool split_rows(const PagedParams& p) {
+  return (long long)p.B * p.Sq * p.Hq < 4000 ||
+         ((long long)p.max_pages << p.page_shift) + p.Sq >= 128;
+}
+template <int D, typename T, typename TC>
+cudaError_t launch(const PagedParams& p, const DevCtl& ctl, cudaStream_t st) {
+  return split_rows(p) ? launch_as<D, T, TC, true>(p, ctl, st)
+                       : launch_as<D, T, TC, false>(p, ctl, st);
 }
 
 template <int D>
