@@ -400,12 +400,12 @@ typedef struct pi_paged_desc {
  *   token_mask   [B or 1, Sq] uint8 or NULL (all valid): only valid tokens are
  *                stored, packed: token t goes to position cache_lens[b] + (valid
  *                tokens before t), the position pi_rope_inplace gives it
- *   lens_out     [B] int32 or NULL: the lengths after the call.  May not be
- *                cache_lens itself (PI_ERR_ARG); written also when Sq == 0
+ *   lens_out     [B] int32 or NULL: the lengths after the call.  May not
+ *                overlap cache_lens (PI_ERR_ARG); written also when Sq == 0
  * Tokens past the page table's room are not stored (PI_ERR_ARG in the status
- * word).  Everything outside the written slots is left as it was.  A page that is written must
- * belong to one sequence of the call.  desc: Hq, window, sinks and
- * softmax_scale are not read; Sq <= 16383.
+ * word).  Everything outside the written slots is left as it was.  A page that
+ * is written must belong to one sequence of the call, and to one of its columns.
+ * desc: Hq, window, sinks and softmax_scale are not read; Sq <= 16383.
  */
 int pi_attn_cache_write(const pi_paged_desc* desc, const void* k_new, const void* v_new,
                         const uint8_t* token_mask, const int32_t* page_table,
@@ -449,7 +449,9 @@ int pi_attn_cache_read(const pi_paged_desc* desc, const void* k_pages, const voi
  * sequence's other rows non-finite too.
  *   workspace    device scratch of pi_attn_paged_workspace_bytes(desc) bytes,
  *                16-byte aligned, contents ignored (NULL when that is 0);
- *                calls that may overlap need distinct workspaces
+ *                calls that may overlap need distinct workspaces.  (Long chunks
+ *                over an 8-bit cache rebuild it there as bf16 when the page
+ *                table reaches over at most 512 MiB of such rows.)
  * Supported: Sq <= 16383, B <= 65535, num_pages * page_size and max_pages *
  * page_size below 2^31 - 2^15.  Runs on tensor cores: bf16, d == 256, Hq / Hkv
  * in {1, 2, 4, 8, 16}; everything else on CUDA cores (fp32 arithmetic).

@@ -122,15 +122,15 @@ def attend(q, k_new, v_new, k_rows, v_rows, ar, seg=None, scale=1.0, window=0, s
         keys = np.concatenate([k_rows[b], k_new[b]])
         vals = np.concatenate([v_rows[b], v_new[b]])
         sees = mask(n, Sq, codes, window, sinks)
-        for i in range(Sq):
-            see = sees[i]
-            if not see.any():
-                continue
-            for h in range(Hq):
-                g = h // (Hq // Hkv)
-                x = scale * (keys[see, g] @ q[b, i, h])
-                m = x.max()
-                w = np.exp(x - m)
-                out[b, i, h] = (w @ vals[see, g]) / w.sum()
-                lse[b, i, h] = m + np.log(w.sum())
+        live = sees.any(1)
+        vals = np.where(sees.any(0)[:, None, None], vals, 0)     # stale rows may hold NaN
+        for h in range(Hq):
+            g = h // (Hq // Hkv)
+            with np.errstate(invalid="ignore", over="ignore"):
+                x = np.where(sees, scale * (q[b, :, h] @ keys[:, g].T), -np.inf)
+            m = np.where(live, x.max(1), 0)
+            w = np.exp(x - m[:, None])
+            z = np.where(live, w.sum(1), 1)
+            out[b, :, h] = (w @ vals[:, g]) / z[:, None]
+            lse[b, :, h] = np.where(live, m + np.log(z), -np.inf)
     return out, lse

@@ -76,9 +76,13 @@ class Cache:
         return self.k, self.v, self.table, self.lens
 
     def rows(self, name, b, n=None):
-        e = getattr(self, name + "_exp")
-        return P.rows(_np(getattr(self, name)), None if e is None else e.cpu().numpy(),
-                      self.table_np, b, int(self.lens_np[b]) if n is None else n)
+        n = int(self.lens_np[b]) if n is None else n
+        pages = self.table_np[b, :-(-n // self.page)]           # only these leave the device
+        at = torch.from_numpy(pages.astype(np.int64)).cuda()
+        pool, e = getattr(self, name), getattr(self, name + "_exp")
+        pool = pool.view(torch.uint8)[at].view(pool.dtype)
+        return P.rows(_np(pool), None if e is None else e[at].cpu().numpy(),
+                      np.arange(len(pages))[None], 0, n)
 
 
 def _rand(rng, shape, dtype, std):
@@ -262,7 +266,7 @@ def test_stale_slots_and_padding_hold_nan(Sq, window, cache):
 
 
 @pytest.mark.parametrize("cache", CACHES)
-@pytest.mark.parametrize("Sq", [1, 40])
+@pytest.mark.parametrize("Sq", [1, 40, 150])
 def test_bad_tables_and_lengths_are_reported(Sq, cache):
     """Out-of-range page ids and lengths are bounded and recorded; other
     sequences keep their results, and nothing past the buffers is touched."""
@@ -405,7 +409,7 @@ def test_write_special_values():
     assert k[0, 9, 0, 3] == float("inf") and (k[0, 9, 0, 4:] == 0).all()
 
 
-@pytest.mark.parametrize("Sq", [1, 2, 5, 40])
+@pytest.mark.parametrize("Sq", [1, 2, 5, 40, 150])
 def test_cached_values_come_through_exactly(Sq):
     """One visible cached key: its probability is 1 and out is its value vector,
     rounded to bf16 only.  Every e4m3 byte and exponents over the range."""
@@ -499,10 +503,10 @@ def test_prefix_then_decoding(cache):
 
 
 @pytest.mark.parametrize("cache", CACHES)
-@pytest.mark.parametrize("Sq", [1, 51])
+@pytest.mark.parametrize("Sq", [1, 51, 150])
 def test_captured_step_follows_the_lengths(Sq, cache):
     """One captured graph of attention and append, replayed while the lengths
-    grow; two graphs with a workspace each, and one after the other."""
+    grow."""
     b = _b()
     rng = np.random.default_rng(32)
     B, Hq, d = 2, 8, 256
@@ -543,7 +547,7 @@ def test_captured_step_follows_the_lengths(Sq, cache):
 
 
 @pytest.mark.parametrize("cache", CACHES)
-@pytest.mark.parametrize("Sq", [1, 9, 70])
+@pytest.mark.parametrize("Sq", [1, 9, 70, 150])
 def test_side_stream_and_repeatability(Sq, cache):
     """Calls on two streams at once, each with its own workspace, give the
     same bits as one call after another."""
@@ -676,3 +680,193 @@ def test_binding_checks():
     with pytest.raises(b.PiAttnError):
         b.pi_attn_paged(q[:, :, :5].contiguous(), kn.expand(1, 1, 1, 256).contiguous(), kn,
                         *c.args(), ar, softmax_scale=0.0, **ok)
+
+
+# ------------------------------------------------------- the ends of the ranges
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("Sq,B", [(9, 130), (150, 66), (1, 300)])
+def test_more_sequences_than_one_launch_schedules(Sq, B, cache):
+    """A last launch of few sequences, one of them long."""
+    lens = [int(x) for x in np.random.default_rng(40).integers(0, 120, B)]
+    lens[-1], lens[3] = 24000 // B + 801, 700
+    _attend(40, lens, Sq, cache, 32, mask="causal")
+
+
+@pytest.mark.parametrize("Hkv", [1, 2])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 20), (1, 0)])
+def test_chunk_with_a_used_workspace(window, sinks, Hkv):
+    """What the workspace held (NaN) does not reach the result."""
+    b = _b()
+    c = Cache(41, [0, 77, 1000, 513], 64, Hkv, 256, E4M3)
+    Sq = 260
+    q = _rand(c.rng, (4, Sq, 8, 256), BF16, 0.25)
+    kn, vn = (_rand(c.rng, (4, Sq, Hkv, 256), BF16, 0.25) for _ in range(2))
+    ar = np.ones(Sq, np.uint8)
+    need = b.pi_attn_paged_workspace_bytes(q, kn, *c.args(), window=window, sinks=sinks, **c.exps())
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+    b.pi_attn_paged(q, kn, vn, *c.args(), torch.from_numpy(ar).cuda(), out=out, lse=lse, workspace=ws,
+                    window=window, sinks=sinks, **c.exps())
+    _check(c, q, kn, vn, ar, None, out, lse, 1.0, window, sinks)
+
+
+@pytest.mark.parametrize("cache", CACHES)
+def test_long_ragged_chunks(cache):
+    _attend(42, [5000, 1, 2500], 300, cache, 256, Hkv=2)
+    _attend(43, [3000, 2999], 520, cache, 16, mask="segments", pad=True, window=700, sinks=9)
+
+
+@pytest.mark.parametrize("cache", [F32, E4M3])
+@pytest.mark.parametrize("window", [0, 11])
+def test_fp32_many_short_rows(cache, window):
+    """Enough rows of few keys that each goes to one warp."""
+    lens = [int(x) for x in np.random.default_rng(44).integers(0, 90, 70)]
+    _attend(44, lens, 16, cache, 16, d=64, Hq=4, Hkv=2, dtype=F32, mask="segments", pad=True,
+            window=window, sinks=2)
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("Sq", [1, 6, 150])
+def test_empty_pool(Sq, d, cache):
+    """No page at all, or no column: only the chunk is seen; a length that
+    claims cached tokens is clamped and recorded."""
+    b = _b()
+    rng = np.random.default_rng(45)
+    q = _rand(rng, (2, Sq, 8, d), BF16, 0.25)
+    kn, vn = (_rand(rng, (2, Sq, 1, d), BF16, 0.25) for _ in range(2))
+    ar = np.ones(Sq, np.uint8)
+    art = torch.from_numpy(ar).cuda()
+    none = [np.zeros((0, 1, d))] * 2
+    ref, _ = P.attend(_np(q), _np(kn), _np(vn), none, none, ar)
+    for pages, columns in ((0, 0), (0, 2), (2, 0)):
+        pool = [torch.zeros(pages, 16, 1, d, device="cuda").to(cache) for _ in range(2)]
+        exps = {}
+        if cache == E4M3:
+            exps = {n: torch.zeros(pages, 16, 1, dtype=torch.uint8, device="cuda")
+                    for n in ("k_exp", "v_exp")}
+        table = torch.zeros(2, columns, dtype=torch.int32, device="cuda")
+        lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+        out = b.pi_attn_paged(q, kn, vn, *pool, table, lens, art, **exps)
+        assert b.pi_attn_read_status() == b.PI_OK
+        assert np.abs(_np(out) - ref).max() <= 3 * 2.0 ** -8 * float(vn.abs().max())
+        k, v, valid = b.pi_attn_cache_read(*pool, table, lens, 3, **exps)
+        assert b.pi_attn_read_status() == b.PI_OK
+        assert (k == 0).all() and (v == 0).all() and (valid == 0).all()
+        out = b.pi_attn_paged(q, kn, vn, *pool, table, lens + 5, art, **exps)
+        assert b.pi_attn_read_status() == b.PI_ERR_ARG
+        assert torch.isfinite(out.float()).all()
+        b.pi_attn_cache_write(kn, vn, *pool, table, lens, **exps)
+        assert b.pi_attn_read_status() == b.PI_ERR_ARG
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (5000, 64), (2 ** 31 - 1, 2 ** 31 - 1)])
+def test_longest_chunk(window, sinks, cache):
+    """16383 new tokens: some rows against a float64 sum on the device."""
+    b = _b()
+    Sq, n = 16383, 1000
+    c = Cache(46, [n], 128, 1, 256, cache)
+    q = _rand(c.rng, (1, Sq, 2, 256), BF16, 0.25)
+    kn, vn = (_rand(c.rng, (1, Sq, 1, 256), BF16, 0.25) for _ in range(2))
+    ar = torch.ones(Sq, dtype=torch.uint8, device="cuda")
+    lse = torch.empty(q.shape[:3], device="cuda")
+    out = b.pi_attn_paged(q, kn, vn, *c.args(), ar, lse=lse, window=window, sinks=sinks, **c.exps())
+    assert b.pi_attn_read_status() == b.PI_OK
+    keys = torch.cat([torch.from_numpy(c.rows("k", 0)[:, 0]).cuda(), kn[0, :, 0].double()])
+    vals = torch.cat([torch.from_numpy(c.rows("v", 0)[:, 0]).cuda(), vn[0, :, 0].double()])
+    x = torch.arange(n + Sq, device="cuda")
+    delta = 2.0 ** -15 * float(q.double().norm(dim=-1).max()) * float(keys.norm(dim=-1).max())
+    vmax = float(vals.abs().max())
+    for i in (0, 1, 127, 128, 5000, 8191, 16000, Sq - 1):
+        s = q[0, i].double() @ keys.T
+        seen = x <= n + i
+        if window:
+            seen &= (n + i - x < window) | (x < sinks)
+        s[:, ~seen] = float("-inf")
+        ref = torch.softmax(s, -1) @ vals
+        err = float((out[0, i].double() - ref).abs().max())
+        assert err <= (2 * 2.0 ** -8 + 2 * delta + 2.0 ** -14) * vmax, (i, err)
+        err = float((lse[0, i].double() - torch.logsumexp(s, -1)).abs().max())
+        assert err <= delta + (n + Sq) * 2.0 ** -22 + 2.0 ** -14, (i, err)
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("Sq", [1, 6, 50, 200])
+def test_padding_alone(Sq, cache):
+    """A batch of padding: zeros and -inf, whatever q, k and v hold."""
+    b = _b()
+    c = Cache(47, [300, 0, 40], 16, 1, 256, cache)
+    q, out = (torch.full((3, Sq, 8, 256), float("nan"), dtype=BF16, device="cuda") for _ in range(2))
+    kn = torch.full((3, Sq, 1, 256), float("nan"), dtype=BF16, device="cuda")
+    lse = torch.zeros(3, Sq, 8, device="cuda")
+    seg = torch.full((Sq,), -1, dtype=torch.int32, device="cuda")
+    ar = torch.ones(Sq, dtype=torch.uint8, device="cuda")
+    b.pi_attn_paged(q, kn, kn, *c.args(), ar, segment_ids=seg, out=out, lse=lse, **c.exps())
+    assert b.pi_attn_read_status() == b.PI_OK
+    assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("Sq", [1, 40, 150])
+def test_two_graphs_at_once(Sq, cache):
+    """Two captured calls, a workspace each, replayed on two streams together."""
+    b = _b()
+    c = Cache(48, [900, 100, 0, 2000], 64, 1, 256, cache)
+    kn, vn = (_rand(c.rng, (4, Sq, 1, 256), BF16, 0.25) for _ in range(2))
+    ar = torch.ones(Sq, dtype=torch.uint8, device="cuda")
+    qs = [_rand(c.rng, (4, Sq, 8, 256), BF16, 0.25) for _ in range(2)]
+    refs = [b.pi_attn_paged(q, kn, vn, *c.args(), ar, **c.exps()) for q in qs]
+    need = b.pi_attn_paged_workspace_bytes(qs[0], kn, *c.args(), **c.exps())
+    outs = [torch.zeros_like(q) for q in qs]
+    spaces = [torch.empty(max(need, 16), dtype=torch.uint8, device="cuda") for _ in qs]
+    graphs, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for q, out, ws in zip(qs, outs, spaces):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(3):
+                b.pi_attn_paged(q, kn, vn, *c.args(), ar, out=out, workspace=ws, **c.exps())
+        graphs.append(g)
+    for _ in range(5):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    assert b.pi_attn_read_status() == b.PI_OK
+    for out, ref in zip(outs, refs):
+        assert torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("Sq", [1, 30, 150])
+def test_one_page_twice_in_a_table(Sq, cache):
+    """A page may stand for several places of one sequence when it is read."""
+    b = _b()
+    c = Cache(49, [96, 64], 16, 1, 256, cache)
+    c.table[0, 3], c.table[0, 4], c.table[1, 2] = c.table[0, 0], c.table[0, 0], c.table[0, 5]
+    c.table_np = c.table.cpu().numpy()
+    q = _rand(c.rng, (2, Sq, 8, 256), BF16, 0.25)
+    kn, vn = (_rand(c.rng, (2, Sq, 1, 256), BF16, 0.25) for _ in range(2))
+    ar = np.ones(Sq, np.uint8)
+    out = b.pi_attn_paged(q, kn, vn, *c.args(), torch.from_numpy(ar).cuda(), **c.exps())
+    _check(c, q, kn, vn, ar, None, out, None, 1.0, 0, 0)
+
+
+def test_binding_checks_of_the_limits():
+    b = _b()
+    c = Cache(50, [10, 5], 16, 1, 256, BF16)
+    q = _rand(c.rng, (2, 1, 8, 256), BF16, 1.0)
+    kn = _rand(c.rng, (2, 1, 1, 256), BF16, 1.0)
+    ar = torch.ones(1, dtype=torch.uint8, device="cuda")
+    for bad in (2 ** 31, 2 ** 32 + 5):
+        with pytest.raises(ValueError):
+            b.pi_attn_paged(q, kn, kn, *c.args(), ar, window=bad)
+        with pytest.raises(ValueError):
+            b.pi_attn_paged(q, kn, kn, *c.args(), ar, window=1, sinks=bad)
+    with pytest.raises(TypeError):
+        b.pi_attn_paged(q, kn, kn, *c.args(), ar, window=2.5)
+    lens = torch.tensor([10, 5, 0], dtype=torch.int32, device="cuda")
+    with pytest.raises(b.PiAttnError):                   # lens_out overlaps cache_lens
+        b.pi_attn_cache_write(kn, kn, c.k, c.v, c.table, lens[:2], lens_out=lens[1:])

@@ -140,6 +140,8 @@ def test_bad_cache_pointers(call):
 def test_write_and_attention_refusals():
     b, L = _lib()
     assert _write(L, _desc(b), lens_out=FAKE) == b.PI_ERR_ARG      # lens_out is cache_lens
+    near = ctypes.c_void_p(FAKE.value + 4)                         # or overlaps it
+    assert _write(L, _desc(b, B=2), lens_out=near) == b.PI_ERR_ARG
     assert _write(L, _desc(b), lens_out=ctypes.c_void_p(0x20002)) == b.PI_ERR_ALIGN
     for call in (_write, _attend):
         assert call(L, _desc(b, mask_batch_stride=15)) == b.PI_ERR_ARG

@@ -15,6 +15,7 @@ Names mirror the C ABI in include/pi_attn.h: ``pi_attn_prefill``,
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import torch
@@ -474,9 +475,13 @@ def _paged_desc(B, Sq, Hq, dtype, k_pages, page_table, window=0, sinks=0, softma
     got = _paged_descs.get(key)
     if got is None:
         n, page, Hkv, d = k_pages.shape
+        window, sinks = operator.index(window), operator.index(sinks)
+        for x in (B, Sq, Hq, Hkv, n, page_table.shape[1], window, sinks):
+            if not -2 ** 31 <= x < 2 ** 31:
+                raise ValueError(f"{x} does not fit the descriptor's 32 bits")
         desc = PiPagedDesc(B, Sq, Hq, Hkv, d, PI_BF16 if dtype == torch.bfloat16 else PI_F32,
                            _CACHE_CODES[k_pages.dtype], page, n, page_table.shape[1],
-                           int(window), int(sinks), float(softmax_scale), 0, mask_stride)
+                           window, sinks, float(softmax_scale), 0, mask_stride)
         ref = ctypes.byref(desc)
         got = (ref, int(lib().pi_attn_paged_workspace_bytes(ref)), desc)
         if len(_paged_descs) >= 1024:
@@ -565,7 +570,7 @@ def pi_attn_cache_write(k_new, v_new, k_pages, v_pages, page_table, cache_lens, 
     uint8 exponents k_exp, v_exp [num_pages,page_size,Hkv]); page_table int32
     [B,max_pages]; cache_lens int32 [B].  Valid tokens (``token_mask`` uint8
     [Sq] or [B,Sq], None = all) go to the positions after cache_lens, packed.
-    ``lens_out`` (int32 [B], not cache_lens) receives the new lengths."""
+    ``lens_out`` (int32 [B], apart from cache_lens) receives the new lengths."""
     if k_new.dim() != 4:
         raise ValueError("k_new must be [B, Sq, Hkv, d]")
     B, Sq, Hkv, d = k_new.shape

@@ -124,7 +124,11 @@ int pi_attn_cache_write(const pi_paged_desc* d, const void* k_new, const void* v
   if (rc != PI_OK) return rc;
   if (d->B == 0) return PI_OK;
   if (d->Sq > 0 && (!k_new || !v_new)) return PI_ERR_ARG;
-  if (lens_out && lens_out == cache_lens) return PI_ERR_ARG;
+  if (lens_out && cache_lens) {              // every CTA reads its sequence's length
+    const uintptr_t x = reinterpret_cast<uintptr_t>(lens_out), n = sizeof(int32_t) * (size_t)d->B;
+    const uintptr_t y = reinterpret_cast<uintptr_t>(cache_lens);
+    if (x < y + n && y < x + n) return PI_ERR_ARG;
+  }
   rc = check_cache(d, k_pages, v_pages, k_exp, v_exp, page_table, cache_lens);
   if (rc != PI_OK) return rc;
   if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(lens_out, 4)) return PI_ERR_ALIGN;
