@@ -18,8 +18,8 @@
 // launch latency (a token per sequence).  d / 8 lanes own one vector, 8
 // elements each (16 bytes of bf16), so a warp access is a contiguous run; the
 // amax is one warp reduction (d / 8 lanes of shuffles below d = 256); a thread
-// keeps the loads of kRows vectors of keys and of values in flight.  Measured: 32
-// prefixes of 824 tokens to e4m3 in 11.8 us (3.4 TB/s; 20 us with the loads behind
+// keeps the loads of several vectors of keys and of values in flight.  Measured: 32
+// prefixes of 824 tokens to e4m3 in 11.5 us (3.5 TB/s; 20 us with the loads behind
 // the slot lookups and the scaling in fp32), four bf16 sequences of up to 16000
 // tokens read back in 17.2 us (6.7 TB/s), a token for each of 32 sequences 2.4 us.
 #include <algorithm>
@@ -32,7 +32,10 @@ namespace piattn {
 namespace {
 
 constexpr int kCacheThreads = 128;
-constexpr int kRows = 4;                    // vectors per thread and tensor
+// Vectors per thread and tensor.  Writing, 32 prefixes of 824 tokens to e4m3 / 8 of
+// 611 in bf16: 1 vector 13.8 / 3.1 us, 2 11.5 / 2.8, 3 11.5 / 2.7, 4 11.8 / 2.9, 8 14.6
+// / 3.1 (more copies in flight against more CTAs).
+constexpr int kWriteRows = 3, kReadRows = 4;
 
 // Eight elements as they lie in memory, and as floats.
 struct F8 { float x[8]; };
@@ -191,10 +194,10 @@ __global__ void __launch_bounds__(kCacheThreads)
   const long long src0 = ((long long)b * p.S + t0) * p.Hkv;
   const TIn* kin = static_cast<const TIn*>(p.k_in);
   const TIn* vin = static_cast<const TIn*>(p.v_in);
-  Raw<TIn> kr[kRows], vr[kRows];
+  Raw<TIn> kr[kWriteRows], vr[kWriteRows];
   auto fetch = [&](int v0) {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+    for (int i = 0; i < kWriteRows; ++i) {
       const int v = v0 + i * vpb + vi;
       if (v < n_vec) {
         load(kin + (src0 + v) * p.d + e0, kr[i]);
@@ -254,10 +257,10 @@ __global__ void __launch_bounds__(kCacheThreads)
 
   TC* kp = static_cast<TC*>(p.kp);
   TC* vp = static_cast<TC*>(p.vp);
-  for (int v0 = 0; v0 < n_vec; v0 += vpb * kRows) {
+  for (int v0 = 0; v0 < n_vec; v0 += vpb * kWriteRows) {
     if (v0 > 0) fetch(v0);
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+    for (int i = 0; i < kWriteRows; ++i) {
       const int v = v0 + i * vpb + vi;
       const int t = p.Hkv == 1 ? v : v / p.Hkv;
       const int slot = v < n_vec ? s_slot[t] : -1;
@@ -335,11 +338,11 @@ __global__ void __launch_bounds__(kCacheThreads)
   const TC* vp = static_cast<const TC*>(p.vp);
   TOut* ko = static_cast<TOut*>(p.k_out);
   TOut* vo = static_cast<TOut*>(p.v_out);
-  for (int v0 = 0; v0 < n_vec; v0 += vpb * kRows) {
-    Raw<TC> kr[kRows], vr[kRows];
-    uint8_t kb[kRows], vb[kRows];
+  for (int v0 = 0; v0 < n_vec; v0 += vpb * kReadRows) {
+    Raw<TC> kr[kReadRows], vr[kReadRows];
+    uint8_t kb[kReadRows], vb[kReadRows];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+    for (int i = 0; i < kReadRows; ++i) {
       const int v = v0 + i * vpb + vi;
       const int t = p.Hkv == 1 ? v : v / p.Hkv;
       const int slot = v < n_vec ? s_slot[t] : -1;
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(kCacheThreads)
       }
     }
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+    for (int i = 0; i < kReadRows; ++i) {
       const int v = v0 + i * vpb + vi;
       if (v >= n_vec || s_slot[p.Hkv == 1 ? v : v / p.Hkv] == -2) continue;
       const long long at = (dst0 + v) * p.d + e0;
@@ -379,11 +382,11 @@ __global__ void __launch_bounds__(kCacheThreads)
   }
 }
 
-// Tokens per CTA: enough vectors that every thread has kRows of each tensor,
+// Tokens per CTA: enough vectors that every thread has `rows` of each tensor,
 // fewer when the grid would leave SMs idle.
-int tokens_per_cta(const CacheParams& p) {
+int tokens_per_cta(const CacheParams& p, int rows) {
   const int vpb = kCacheThreads / (p.d >> 3);
-  int tok = (vpb * kRows + p.Hkv - 1) / p.Hkv;
+  int tok = (vpb * rows + p.Hkv - 1) / p.Hkv;
   tok = std::min(std::max(tok, 1), kCacheMaxTok);
   while (tok > 1 && (long long)p.B * ((p.S + tok - 1) / tok) < 2 * sm_count()) tok = (tok + 1) / 2;
   return tok;
@@ -392,7 +395,7 @@ int tokens_per_cta(const CacheParams& p) {
 // (Pools and dense tensors share a type unless the pool is e4m3.)
 template <typename T, typename TC>
 cudaError_t launch(const CacheParams& p, bool write, const DevCtl& ctl, cudaStream_t st) {
-  const int tok = tokens_per_cta(p);
+  const int tok = tokens_per_cta(p, write ? kWriteRows : kReadRows);
   dim3 grid((unsigned)((p.S + tok - 1) / tok), (unsigned)p.B);
   return write ? launch_pdl(cache_write_kernel<T, TC>, grid, dim3(kCacheThreads), 0, st, p, ctl, tok)
                : launch_pdl(cache_read_kernel<T, TC>, grid, dim3(kCacheThreads), 0, st, p, ctl, tok);

@@ -10,9 +10,9 @@
 //    alike: each sequence's tiles in equal pieces of at most `per`, one CTA a piece,
 //    or, with more sequences than half the CTAs, all tiles in a row in equal
 //    ranges.  (A CTA whose range crosses into another sequence starts over with its
-//    queries: 4 us of 12 at 32 sequences of 880 tokens.)  A CTA's four warps take its tiles in turn, each through its own
-//    16-key stage: one TMA box per tile and operand, K refilled as soon as the
-//    scores are done, V as soon as the product is.
+//    queries: 4 us of 12 at 32 sequences of 880 tokens.)  A CTA's four warps take its
+//    tiles in turn, each through its own 16-key stage: one TMA box per tile and
+//    operand, K refilled as soon as the scores are done, V as soon as the product is.
 //  * Scores transposed, S^T = K Q^T by mma.m16n8k16, so that the 8 query rows
 //    fill the n8 side; an fp32 online softmax per query column; O^T += V^T P^T,
 //    P^T by an in-register 8x8 transpose.
@@ -30,8 +30,13 @@
 // The chunk's own keys (at most 8) are one more, cheap tile: a short loop of dot
 // products while the first copies are in flight, kept as a fifth warp's partial.
 // Code is kept short throughout: a small call waits for its instructions more
-// than for its data.  Rows that no query sees are zeroed (bf16: in V's tile; e4m3: by their scale), so
-// that what a stale slot holds (NaN) does not reach the result.
+// than for its data.  Rows that no query sees are zeroed (bf16: in V's tile; e4m3:
+// by their scale), so that what a stale slot holds (NaN) does not reach the result.
+//
+// Measured, both launches: one token of 16 sequences of 12000 to 16000 bf16 tokens
+// 48.6 us (4.7 TB/s, of 6.5 that a copy reaches), of 32 sequences of 400 to 880 e4m3
+// tokens 15.3 us, of one of 880 tokens 9.4 us.  Short calls are a chain of waits:
+// launch, plan, queries and first tiles, merge, the second launch.
 #include <cfloat>
 #include <cstddef>
 

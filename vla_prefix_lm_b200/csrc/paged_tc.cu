@@ -50,6 +50,13 @@
 // of up to 512 chunk tokens (longer chunks: in the workspace).
 // Every wait is bounded (DevCtl); counters that index barriers and ring slots
 // run across segments.
+//
+// Measured: 512 tokens x 8 heads against four bf16 sequences of 15000 tokens 231 us
+// (1144 TFLOP/s of 1655), against e4m3 ones 247 us (the rebuilding pass and fp32
+// partials included); 51 tokens of 32 sequences of 816 tokens 27.6 us, the smallest
+// call 12.4 us.  A tile takes about 4000 cycles where its MMAs need 2048: the
+// softmax warps' chain (score read, maxima met across the pair of warps, 1024 cycles
+// of exponentials, P stored) bounds it, the MMAs wait.
 #include <cfloat>
 
 #include "launch.h"
