@@ -229,11 +229,12 @@ def test_sharp_scores(Sq, cache):
 @pytest.mark.parametrize("cache", CACHES)
 @pytest.mark.parametrize("Sq", [1, 3, 60, 260])
 @pytest.mark.parametrize("window", [0, 37])
-def test_stale_slots_and_padding_hold_nan(Sq, window, cache):
+@pytest.mark.parametrize("room", [40, 17000])
+def test_stale_slots_and_padding_hold_nan(Sq, window, cache, room):
     """NaN and infinities in every slot that no query sees, and in padding
     tokens' q, k and v, do not reach the result."""
     lens = [200, 0, 77]
-    c = Cache(14, lens, 16, 1, 256, cache, room=40)
+    c = Cache(14, lens, 16, 1, 256, cache, room=room)
     rng, B = c.rng, 3
     q = _rand(rng, (B, Sq, 8, 256), BF16, 0.25)
     kn, vn = (_rand(rng, (B, Sq, 1, 256), BF16, 0.25) for _ in range(2))
@@ -267,11 +268,12 @@ def test_stale_slots_and_padding_hold_nan(Sq, window, cache):
 
 @pytest.mark.parametrize("cache", CACHES)
 @pytest.mark.parametrize("Sq", [1, 40, 150])
-def test_bad_tables_and_lengths_are_reported(Sq, cache):
+@pytest.mark.parametrize("room", [0, 17000])
+def test_bad_tables_and_lengths_are_reported(Sq, cache, room):
     """Out-of-range page ids and lengths are bounded and recorded; other
     sequences keep their results, and nothing past the buffers is touched."""
     b = _b()
-    c = Cache(15, [100, 90, 60], 16, 1, 256, cache)
+    c = Cache(15, [100, 90, 60], 16, 1, 256, cache, room=room)
     rng = c.rng
     q = _rand(rng, (3, Sq, 8, 256), BF16, 0.25)
     kn, vn = (_rand(rng, (3, Sq, 1, 256), BF16, 0.25) for _ in range(2))
@@ -410,11 +412,12 @@ def test_write_special_values():
 
 
 @pytest.mark.parametrize("Sq", [1, 2, 5, 40, 150])
-def test_cached_values_come_through_exactly(Sq):
+@pytest.mark.parametrize("room", [0, 17000])
+def test_cached_values_come_through_exactly(Sq, room):
     """One visible cached key: its probability is 1 and out is its value vector,
     rounded to bf16 only.  Every e4m3 byte and exponents over the range."""
     b = _b()
-    c = Cache(24, [32], 32, 1, 256, E4M3)
+    c = Cache(24, [32], 32, 1, 256, E4M3, room=room)
     bits = torch.arange(256, dtype=torch.uint8)
     bits[0x7F] = bits[0xFF] = 0
     slot = P.slot(c.table_np, 0, 0, 32)
@@ -810,10 +813,11 @@ def test_padding_alone(Sq, cache):
 
 @pytest.mark.parametrize("cache", CACHES)
 @pytest.mark.parametrize("Sq", [1, 40, 150])
-def test_two_graphs_at_once(Sq, cache):
+@pytest.mark.parametrize("room", [0, 17000])
+def test_two_graphs_at_once(Sq, cache, room):
     """Two captured calls, a workspace each, replayed on two streams together."""
     b = _b()
-    c = Cache(48, [900, 100, 0, 2000], 64, 1, 256, cache)
+    c = Cache(48, [900, 100, 0, 2000], 64, 1, 256, cache, room=room)
     kn, vn = (_rand(c.rng, (4, Sq, 1, 256), BF16, 0.25) for _ in range(2))
     ar = torch.ones(Sq, dtype=torch.uint8, device="cuda")
     qs = [_rand(c.rng, (4, Sq, 8, 256), BF16, 0.25) for _ in range(2)]
@@ -870,3 +874,19 @@ def test_binding_checks_of_the_limits():
     lens = torch.tensor([10, 5, 0], dtype=torch.int32, device="cuda")
     with pytest.raises(b.PiAttnError):                   # lens_out overlaps cache_lens
         b.pi_attn_cache_write(kn, kn, c.k, c.v, c.table, lens[:2], lens_out=lens[1:])
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("window", [0, 5200])
+@pytest.mark.parametrize("lens,Sq,Hq,Hkv", [
+    ([9000], 1, 8, 1),                         # long for its number of units
+    ([12000, 5], 4, 4, 2),
+    ([17000] + [3] * 20, 1, 8, 1),
+    (list(range(0, 520, 4)), 1, 16, 2),        # more units than half the CTAs
+    ([100] * 55, 2, 4, 1),                     # the most units that clusters take
+    ([100] * 56, 2, 4, 1),
+])
+def test_decode_forms(lens, Sq, Hq, Hkv, window, cache):
+    """Every way the few-row kernel shares out its work."""
+    _attend(51, lens, Sq, cache, 64, Hq=Hq, Hkv=Hkv, mask="segments", pad=True, window=window,
+            sinks=7, batch_mask=True)

@@ -27,16 +27,19 @@
 //    whole is written out; the others leave fp32 partials that a second kernel
 //    merges by the log-sum-exp rule.  No atomics: the result does not depend on
 //    timing.
+//  * When all sequences' clusters fit at once and none is very long (clustered()),
+//    a cluster of eight CTAs takes a sequence instead, in equal pieces, and merges
+//    their partials over distributed shared memory: no plan, no second launch.
 // The chunk's own keys (at most 8) are one more, cheap tile: a short loop of dot
 // products while the first copies are in flight, kept as a fifth warp's partial.
 // Code is kept short throughout: a small call waits for its instructions more
 // than for its data.  Rows that no query sees are zeroed (bf16: in V's tile; e4m3:
 // by their scale), so that what a stale slot holds (NaN) does not reach the result.
 //
-// Measured, both launches: one token of 16 sequences of 12000 to 16000 bf16 tokens
-// 48.6 us (4.7 TB/s, of 6.5 that a copy reaches), of 32 sequences of 400 to 880 e4m3
-// tokens 15.3 us, of one of 880 tokens 9.4 us.  Short calls are a chain of waits:
-// launch, plan, queries and first tiles, merge, the second launch.
+// Measured: one token of 16 sequences of 12000 to 16000 bf16 tokens 44.0 us (5.2
+// TB/s, of 6.5 that a copy reaches; 49.3 in two launches), of 32 sequences of 400 to
+// 880 e4m3 tokens 11.5 us (15.3), of one of 880 tokens 7.9 us (9.6).  Short calls are
+// a chain of waits: launch, length, page, first tiles, merge.
 #include <cfloat>
 #include <cstddef>
 
@@ -54,6 +57,7 @@ constexpr int kD = 256;
 constexpr int kTile = 16;
 constexpr int kPartStride = kD + 4;         // fp32 partial rows: 4-bank skew
 constexpr int kGroup = kPagedDecodeGroup;
+constexpr int kClusterCtas = 8;                // CTAs of a cluster that shares a unit
 constexpr int kPerSm = 3;                   // CTAs per SM (164 registers a thread)
 
 template <bool kE4M3>
@@ -77,14 +81,17 @@ struct Smem {
   float m[kWarps + 1][kRows];               // [kWarps]: the chunk's own keys
   float l[kWarps + 1][kRows];
   alignas(16) float o_chunk[kRows][kD];
+  float2 own[kRows];                        // this CTA's (m, l) for its cluster
   uint64_t k_full[kWarps], v_full[kWarps];
   int abort;
 };
 
-static_assert(offsetof(Smem, o_chunk) % 16 == 0 && Cfg<true>::kBody % 16 == 0 &&
+static_assert(offsetof(Smem, o_chunk) % 16 == 0 && offsetof(Smem, own) % 8 == 0 &&
+                  Cfg<true>::kBody % 16 == 0 &&
                   Cfg<false>::kBody % 16 == 0 && offsetof(Smem, k_full) % 8 == 0,
               "vector accesses need aligned places");
 
+static_assert(kPerSm * (Cfg<false>::kBody + (int)sizeof(Smem) + 2048) <= 228 * 1024, "per SM");
 template <bool kE4M3>
 constexpr int smem_bytes() { return Cfg<kE4M3>::kBody + (int)sizeof(Smem) + 1024; }
 
@@ -225,7 +232,16 @@ __device__ __forceinline__ uint32_t chunk_off(int j, int c) {
   return (uint32_t)((c >> 7) * (kTile * 128) + j * 128 + ((((c >> 4) & 7) ^ (j & 7)) << 4));
 }
 
-template <bool kE4M3>
+__device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// kCluster: the eight CTAs of a cluster read one unit in equal pieces and merge on
+// chip.  Else CTAs follow the plan and leave partials to paged_decode_merge.
+template <bool kE4M3, bool kCluster>
 __global__ void __launch_bounds__(kThreads, kPerSm)
     paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const DevCtl ctl) {
   using C = Cfg<kE4M3>;
@@ -247,13 +263,20 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
   }
   pdl_wait();
   pdl_launch_dependents();
-  make_plan(p, ctl, sm.plan);
-  const int per = sm.plan.per, total = sm.plan.cum[p.nb];
-  const bool pieces = sm.plan.pieces;
   const int cta = (int)blockIdx.x;
-  // Tiles [pos, end) of all, or this CTA's piece.
-  int pos = pieces ? cta : (int)min((long long)cta * per, (long long)total);
-  const int end = pieces ? min(cta + 1, total) : min(pos + per, total);
+  int per = 0, pos = 0, end = 1;
+  bool pieces = true;
+  if constexpr (kCluster) {
+    __syncthreads();                                  // the barriers exist
+  } else {
+    make_plan(p, ctl, sm.plan);
+    per = sm.plan.per;
+    pieces = sm.plan.pieces;
+    const int total = sm.plan.cum[p.nb];
+    // Tiles [pos, end) of all, or this CTA's piece.
+    pos = pieces ? cta : (int)min((long long)cta * per, (long long)total);
+    end = pieces ? min(cta + 1, total) : min(pos + per, total);
+  }
   const int R = p.Sq * p.G;
   const float sl2 = p.scale_log2;
   const uint32_t kt = smem_u32(ring + warp * 2 * C::kBytes), vt = kt + C::kBytes;
@@ -262,13 +285,20 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
 
   while (pos < end) {
     // ------------------------------------------------- the segment
-    const int b = find_seq(sm.plan, p.nb, pos);
-    const int len = sm.plan.len[b];
+    const int b = kCluster ? cta / kClusterCtas / p.Hkv : find_seq(sm.plan, p.nb, pos);
+    const int len = kCluster ? cached_len(p.lens, b, p.max_pages, p.page_shift, bad)
+                             : sm.plan.len[b];
     const Seen sn = seen_tiles(p, len);
     const int unit_tiles = sn.count + 1;
-    const int rem = pos - sm.plan.cum[b];
+    const int rem = kCluster ? cta / kClusterCtas % p.Hkv : pos - sm.plan.cum[b];
     int h, i0, i1;
-    if (pieces) {
+    if constexpr (kCluster) {
+      const int c = cta % kClusterCtas;
+      h = rem;
+      i0 = (int)((long long)c * unit_tiles / kClusterCtas);
+      i1 = (int)((long long)(c + 1) * unit_tiles / kClusterCtas);
+      ++pos;
+    } else if (pieces) {
       const int n = (unit_tiles + per - 1) / per;
       h = rem / n;
       i0 = (int)((long long)(rem - h * n) * unit_tiles / n);
@@ -673,7 +703,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
           acc[k].w += f * x.w;
         }
       }
-      if (r < R) {
+      if constexpr (kCluster) {
+        __syncthreads();                              // the warps' partials have been read
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<float4*>(opart + r * kD + c0 + 64 * k) = acc[k];
+        if (c0 == 0) sm.own[r] = make_float2(M, L);
+      } else if (r < R) {
         if (i0 == 0 && i1 == unit_tiles) {
           const float inv = L > 0.f ? 1.f / L : (L == L ? 0.f : L);
           const long long row = ((long long)bb * p.Sq + (r >> p.g_shift)) * p.Hq +
@@ -703,6 +739,45 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     __syncthreads();
   }
   if (bad) record_status(ctl, kStatusArg);
+  if constexpr (kCluster) {
+    // CTA c merges columns [32 c, 32 c + 32) of the eight partials: thread t row
+    // t / 16, two columns.
+    if (sm.abort && t < kRows) sm.own[t] = make_float2(-INFINITY, 0.f);
+    __syncwarp();
+    cluster_sync();
+    const int r = t >> 4, c = cta % kClusterCtas, col = 32 * c + (t & 15) * 2;
+    const int b = cta / kClusterCtas / p.Hkv, h = cta / kClusterCtas % p.Hkv;
+    const uint32_t src = smem_u32(opart + r * kD + col), own = smem_u32(&sm.own[r]);
+    float2 ml[kClusterCtas], x[kClusterCtas];
+#pragma unroll
+    for (int k = 0; k < kClusterCtas; ++k) {
+      ml[k] = ld_cluster_f32x2(mapa_shared(own, (uint32_t)k));
+      x[k] = ld_cluster_f32x2(mapa_shared(src, (uint32_t)k));
+    }
+    float M = -INFINITY, L = 0.f, a0 = 0.f, a1 = 0.f;
+#pragma unroll
+    for (int k = 0; k < kClusterCtas; ++k) M = fmaxf(M, ml[k].y > 0.f ? ml[k].x : -INFINITY);
+#pragma unroll
+    for (int k = 0; k < kClusterCtas; ++k) {
+      if (ml[k].y == 0.f) continue;                   // no visible key
+      const float w = ml[k].y > 0.f ? ex2(ml[k].x - M) : 1.f;    // NaN goes on
+      L += w * ml[k].y;
+      a0 += w * x[k].x;
+      a1 += w * x[k].y;
+    }
+    if (r < R) {
+      const float inv = L > 0.f ? 1.f / L : (L == L ? 0.f : L);
+      const long long row = ((long long)b * p.Sq + (r >> p.g_shift)) * p.Hq + (long long)h * p.G +
+                            (r & (p.G - 1));
+      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + row * kD + col) =
+          cvt_bf16x2(a0 * inv, a1 * inv);
+      if (p.lse && col == 0)
+        p.lse[row] =
+            L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : (L == L ? -INFINITY : L);
+    }
+    __syncwarp();
+    cluster_sync();                                   // the others may still read this CTA's
+  }
   // After a timeout: a bounded wait for this warp's copies in flight.
   if (stuck && lane == 0) {
     (void)mbar_wait(&sm.k_full[warp], n_load & 1, ctl);
@@ -807,19 +882,44 @@ int group_size(const PagedParams& p) {
   return (int)min(n, (long long)kGroup);
 }
 
-template <bool kE4M3>
+template <bool kE4M3, bool kCluster>
 cudaError_t launch(const PagedDecodeParams& p, const DevCtl& ctl, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<kE4M3>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+  auto* kernel = paged_decode_kernel<kE4M3, kCluster>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              smem_bytes<kE4M3>());
   if (e != cudaSuccess) return e;
   // Three CTAs an SM need the whole carve-out.
-  const cudaError_t c = cudaFuncSetAttribute(paged_decode_kernel<kE4M3>,
-                                             cudaFuncAttributePreferredSharedMemoryCarveout,
-                                             cudaSharedmemCarveoutMaxShared);
+  const cudaError_t c = cudaFuncSetAttribute(
+      kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (c != cudaSuccess) return c;
-  return launch_pdl(paged_decode_kernel<kE4M3>, dim3((unsigned)p.n_ctas), dim3(kThreads),
-                    (size_t)smem_bytes<kE4M3>(), st, p, ctl);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.n_ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)smem_bytes<kE4M3>();
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {kClusterCtas, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = kCluster ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, ctl);
+}
+
+// Whether a cluster takes each unit: all clusters are resident at once, and the
+// longest cache that the page table can hold is neither too long for eight CTAs nor,
+// with few units, worth spreading over more.  Measured, split in two launches / a
+// cluster each, bf16, lengths from half to all of the stated one: 1 sequence of 880
+// 10.4 / 8.3 us, 4000 12.3 / 11.7, 8000 14.3 / 15.3; 4 of 8000 22.6 / 20.5; 16 of 880
+// 13.0 / 9.5, 8000 30 / 25; 32 of 880 14.7 / 11.5, 8000 43 / 39; 64 of 880 19.7 / 22.7,
+// 128 of 880 27 / 34.
+bool clustered(const PagedParams& p) {
+  const long long units = (long long)p.B * p.Hkv;
+  long long n = (long long)p.max_pages << p.page_shift;
+  if (p.window > 0) n = min(n, (long long)p.window + p.sinks);
+  return units * kClusterCtas <= (long long)sm_count() * kPerSm &&
+         n <= min(5000 * units, 16384ll);
 }
 
 }  // namespace
@@ -831,7 +931,8 @@ bool paged_decode_applies(const PagedParams& p) {
          p.num_pages > 0 && group_size(p) >= 1;
 }
 
-size_t paged_decode_workspace_bytes(const PagedParams&) {
+size_t paged_decode_workspace_bytes(const PagedParams& p) {
+  if (clustered(p)) return 0;
   return (size_t)sm_count() * kPerSm * 2 * kRows * (kD + 2) * sizeof(float);
 }
 
@@ -847,12 +948,17 @@ cudaError_t launch_paged_decode(const PagedParams& a, float* ws, const DevCtl& c
   const bool e4 = a.cache_dtype == kCacheE4M3;
   if (!encode_pool(&p.map_k, a.kp, a, e4) || !encode_pool(&p.map_v, a.vp, a, e4))
     return cudaErrorUnknown;
+  if (clustered(a)) {
+    p.nb = a.B;
+    p.n_ctas = a.B * a.Hkv * kClusterCtas;
+    return e4 ? launch<true, true>(p, ctl, st) : launch<false, true>(p, ctl, st);
+  }
   const int group = group_size(a);
   for (int b0 = 0; b0 < a.B; b0 += group) {
     p.b0 = b0;
     p.nb = min(group, a.B - b0);
     p.n_ctas = sm_count() * kPerSm;
-    const cudaError_t e = e4 ? launch<true>(p, ctl, st) : launch<false>(p, ctl, st);
+    const cudaError_t e = e4 ? launch<true, false>(p, ctl, st) : launch<false, false>(p, ctl, st);
     if (e != cudaSuccess) return e;
     const cudaError_t m = launch_pdl(paged_decode_merge,
                                      dim3((unsigned)(p.nb * a.Hkv), (unsigned)(a.Sq * p.G)),
