@@ -433,7 +433,8 @@ int pi_attn_cache_read(const pi_paged_desc* desc, const void* k_pages, const voi
  *   q            [B, Sq, Hq, d];  k_new, v_new [B, Sq, Hkv, d]
  *   ar_mask      [B or 1, Sq] uint8 (all nonzero: causal among the new tokens)
  *   segment_ids  [B or 1, Sq] int32 or NULL, as in pi_attn_suffix_masked
- *   out          [B, Sq, Hq, d]; lse [B, Sq, Hq] fp32 or NULL (natural log)
+ *   out          [B, Sq, Hq, d], may be q itself; lse [B, Sq, Hq] fp32 or NULL
+ *                (natural log)
  * Query i of sequence b sees the cached keys [0, cache_lens[b]) and the new
  * keys by the block-index rule.  The new tokens need not be in the cache: the
  * call reads positions below cache_lens only, so it may run before or after

@@ -890,3 +890,45 @@ def test_decode_forms(lens, Sq, Hq, Hkv, window, cache):
     """Every way the few-row kernel shares out its work."""
     _attend(51, lens, Sq, cache, 64, Hq=Hq, Hkv=Hkv, mask="segments", pad=True, window=window,
             sinks=7, batch_mask=True)
+
+
+@pytest.mark.parametrize("d,Hq", [(32, 1), (64, 3)])
+def test_fp32_long_chunk(d, Hq):
+    """A chunk whose codes take more shared memory than a kernel has by default."""
+    b = _b()
+    Sq, n = 9001, 21
+    c = Cache(52, [n], 16, 1, d, F32)
+    q = _rand(c.rng, (1, Sq, Hq, d), F32, d ** -0.25)
+    kn, vn = (_rand(c.rng, (1, Sq, 1, d), F32, d ** -0.25) for _ in range(2))
+    ar = torch.ones(Sq, dtype=torch.uint8, device="cuda")
+    lse = torch.empty(q.shape[:3], device="cuda")
+    out = b.pi_attn_paged(q, kn, vn, *c.args(), ar, lse=lse)
+    assert b.pi_attn_read_status() == b.PI_OK
+    keys = torch.cat([torch.from_numpy(c.rows("k", 0)[:, 0]).cuda(), kn[0, :, 0].double()])
+    vals = torch.cat([torch.from_numpy(c.rows("v", 0)[:, 0]).cuda(), vn[0, :, 0].double()])
+    delta = 2.0 ** -15 * float(q.double().norm(dim=-1).max()) * float(keys.norm(dim=-1).max())
+    vmax = float(vals.abs().max())
+    for i in (0, 3, 4500, Sq - 1):
+        s = q[0, i].double() @ keys[:n + i + 1].T
+        ref = torch.softmax(s, -1) @ vals[:n + i + 1]
+        err = float((out[0, i].double() - ref).abs().max())
+        assert err <= (2 * delta + (n + Sq) * 2.0 ** -22 + 2.0 ** -14) * vmax, (i, err)
+        err = float((lse[0, i].double() - torch.logsumexp(s, -1)).abs().max())
+        assert err <= delta + (n + Sq) * 2.0 ** -22 + 2.0 ** -14, (i, err)
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("Sq", [1, 40, 150])
+@pytest.mark.parametrize("room", [0, 17000])
+def test_out_in_place_of_q(Sq, cache, room):
+    """The result may replace the queries."""
+    b = _b()
+    c = Cache(53, [900, 100, 0, 2000], 64, 1, 256, cache, room=room)
+    q = _rand(c.rng, (4, Sq, 8, 256), BF16, 0.25)
+    kn, vn = (_rand(c.rng, (4, Sq, 1, 256), BF16, 0.25) for _ in range(2))
+    ar = torch.ones(Sq, dtype=torch.uint8, device="cuda")
+    ref = b.pi_attn_paged(q, kn, vn, *c.args(), ar, **c.exps())
+    for _ in range(3):
+        x = q.clone()
+        b.pi_attn_paged(x, kn, vn, *c.args(), ar, out=x, **c.exps())
+        assert torch.equal(x, ref)
