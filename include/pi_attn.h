@@ -453,8 +453,8 @@ int pi_attn_cache_read(const pi_paged_desc* desc, const void* k_pages, const voi
  *                calls that may overlap need distinct workspaces.  (Long chunks
  *                over an 8-bit cache rebuild it there as bf16 when the page
  *                table reaches over at most 512 MiB of such rows.)
- * Supported: Sq <= 16383, B <= 65535, num_pages * page_size and max_pages *
- * page_size below 2^31 - 2^15.  Runs on tensor cores: bf16, d == 256, Hq / Hkv
+ * Supported: Sq <= 16383, B <= 65535, Sq * Hq, num_pages * page_size and
+ * max_pages * page_size below 2^31 - 2^15.  Runs on tensor cores: bf16, d == 256, Hq / Hkv
  * in {1, 2, 4, 8, 16}; everything else on CUDA cores (fp32 arithmetic).
  * Errors (all three calls): PI_ERR_ARG, PI_ERR_ALIGN (dense tensors, pools and
  * workspace 16 bytes; int32 and fp32 arrays 4), PI_ERR_UNSUPPORTED before

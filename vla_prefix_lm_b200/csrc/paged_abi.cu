@@ -78,7 +78,8 @@ int check_attn(const pi_paged_desc* d) {
   if (rc != PI_OK) return rc;
   if (d->Hq <= 0 || d->Hq % d->Hkv != 0 || d->window < 0 || d->sinks < 0) return PI_ERR_ARG;
   if (!std::isfinite(d->softmax_scale) || !(d->softmax_scale > 0.f)) return PI_ERR_ARG;
-  if ((long long)d->Sq * d->Hq >= (1ll << 31)) return PI_ERR_UNSUPPORTED;
+  // (Kernels step a 32-bit row index past a sequence's last row.)
+  if ((long long)d->Sq * d->Hq >= (1ll << 31) - (1ll << 15)) return PI_ERR_UNSUPPORTED;
   return check_mask_stride(d);
 }
 
