@@ -4,7 +4,13 @@ pointer below is fake and never dereferenced).
 """
 
 import ctypes
+import os
+import shutil
+import subprocess
 
+import pytest
+
+from conftest import ROOT
 from test_paged_host import _attend, _desc, _lib
 
 
@@ -16,3 +22,67 @@ def test_rows_that_a_loop_of_32_bits_cannot_count_are_refused():
         d = _desc(b, B=1, Sq=Sq, Hq=Hq, d=32)
         assert L.pi_attn_paged_workspace_bytes(ctypes.byref(d)) == 0
         assert _attend(L, d) == b.PI_ERR_UNSUPPORTED
+
+
+STAGE_CHECK = r"""
+#include <cstdio>
+#include "stage.h"
+using piattn::Stuck;
+
+// A barrier as try_wait.parity sees it: done(p) holds once the phase of parity p
+// before the one under way is complete.
+struct Bar {
+  int issued = 0, landed = 0;
+  bool done(unsigned p) const { return ((unsigned)landed & 1u) != p; }
+};
+
+// The warp's loop over `tiles` tiles, stopped at the wait for K (which 0) or V (1)
+// of tile `at`.  Whether the parities handed back wait for every copy under way.
+static bool waits_for_all(int tiles, int at, int which) {
+  Bar k, v;
+  k.issued = v.issued = 1;
+  Stuck stuck = Stuck::kNo;
+  unsigned used = 0;
+  for (int i = 0; i < tiles; ++i) {
+    const bool more = i + 1 < tiles;
+    if (i == at && which == 0) { stuck = Stuck::kAtK; break; }
+    k.landed = k.issued;
+    if (more) ++k.issued;
+    if (i == at && which == 1) { stuck = more ? Stuck::kAtVAhead : Stuck::kAtV; break; }
+    v.landed = v.issued;
+    ++used;
+    if (more) ++v.issued;
+  }
+  const piattn::StagePhases last = piattn::last_phases(used, stuck);
+  // a wait must not be over while a copy is under way, and must end with it
+  const bool k_open = k.issued > k.landed, v_open = v.issued > v.landed;
+  if (k_open == k.done(last.k) || v_open == v.done(last.v)) return false;
+  k.landed = k.issued;
+  v.landed = v.issued;
+  return k.done(last.k) && v.done(last.v);
+}
+
+int main() {
+  for (int tiles = 1; tiles < 9; ++tiles)
+    for (int at = 0; at < tiles; ++at)
+      for (int which = 0; which < 2; ++which)
+        if (!waits_for_all(tiles, at, which)) {
+          std::printf("tile %d of %d, wait %d\n", at, tiles, which);
+          return 1;
+        }
+  std::printf("stage ok\n");
+}
+"""
+
+
+def test_a_stopped_warp_waits_for_its_last_copies(tmp_path):
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no C++ compiler")
+    src, exe = tmp_path / "stage.cc", tmp_path / "stage"
+    src.write_text(STAGE_CHECK)
+    csrc = os.path.join(ROOT, "vla_prefix_lm_b200", "csrc")
+    subprocess.run([gxx, "-std=c++17", "-Wall", "-Werror", "-I", csrc, str(src), "-o", str(exe)],
+                   check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and "stage ok" in r.stdout, r.stdout

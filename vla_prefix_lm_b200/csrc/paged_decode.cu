@@ -45,6 +45,7 @@
 
 #include "launch.h"
 #include "paged.cuh"
+#include "stage.h"
 
 namespace piattn {
 
@@ -281,7 +282,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
   const float sl2 = p.scale_log2;
   const uint32_t kt = smem_u32(ring + warp * 2 * C::kBytes), vt = kt + C::kBytes;
   uint32_t n_load = 0;                                // tiles this warp has loaded by TMA
-  bool bad = false, stuck = false;
+  bool bad = false;
+  Stuck stuck = Stuck::kNo;
 
   while (pos < end) {
     // ------------------------------------------------- the segment
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
       }
       if (!__all_sync(0xffffffffu, mbar_wait(&sm.k_full[warp], n_load & 1, ctl))) {
         sm.abort = 1;
-        stuck = true;
+        stuck = Stuck::kAtK;
         break;
       }
       // sc[0]: key g, row qr0; [1]: g, qr1; [2], [3]: key g + 8.
@@ -604,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
       const uint32_t pb_hi = movm_trans(cvt_bf16x2(pb0, pb1));
       if (!__all_sync(0xffffffffu, mbar_wait(&sm.v_full[warp], n_load & 1, ctl))) {
         sm.abort = 1;
-        stuck = true;
+        stuck = more ? Stuck::kAtVAhead : Stuck::kAtV;
         break;
       }
       if constexpr (kE4M3) {
@@ -779,9 +781,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     cluster_sync();                                   // the others may still read this CTA's
   }
   // After a timeout: a bounded wait for this warp's copies in flight.
-  if (stuck && lane == 0) {
-    (void)mbar_wait(&sm.k_full[warp], n_load & 1, ctl);
-    (void)mbar_wait(&sm.v_full[warp], n_load & 1, ctl);
+  if (stuck != Stuck::kNo && lane == 0) {
+    const StagePhases last = last_phases(n_load, stuck);
+    (void)mbar_wait(&sm.k_full[warp], last.k, ctl);
+    (void)mbar_wait(&sm.v_full[warp], last.v, ctl);
   }
 }
 
