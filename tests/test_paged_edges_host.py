@@ -8,7 +8,9 @@ import os
 import shutil
 import subprocess
 
+import numpy as np
 import pytest
+import torch
 
 from conftest import ROOT
 from test_paged_host import _attend, _desc, _lib
@@ -86,3 +88,41 @@ def test_a_stopped_warp_waits_for_its_last_copies(tmp_path):
                    check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0 and "stage ok" in r.stdout, r.stdout
+
+
+# -------------------------------------------- what the binding keeps between calls
+
+def _descriptor(b, **kw):
+    """The descriptor that a call with these arguments would pass."""
+    pages = torch.empty(4, 16, 1, 256, dtype=torch.bfloat16)
+    table = torch.empty(2, 3, dtype=torch.int32)
+    return b._paged_desc(2, 5, 8, torch.bfloat16, pages, table, **kw)[2]
+
+
+def test_a_scale_changed_in_place_is_a_new_scale(monkeypatch):
+    b, _ = _lib()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    scale, window, sinks = torch.tensor(0.5), torch.tensor(7), np.array(3)
+    d = _descriptor(b, softmax_scale=scale, window=window, sinks=sinks)
+    assert (d.softmax_scale, d.window, d.sinks) == (0.5, 7, 3)
+    scale.mul_(0.5)
+    window.add_(2)
+    sinks += 1
+    d = _descriptor(b, softmax_scale=scale, window=window, sinks=sinks)
+    assert (d.softmax_scale, d.window, d.sinks) == (0.25, 9, 4)
+    assert _descriptor(b, softmax_scale=0.25, window=9, sinks=4) is d
+
+
+def test_refusals_do_not_depend_on_earlier_calls(monkeypatch):
+    b, _ = _lib()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    for _ in range(2):
+        _descriptor(b, window=2, sinks=1)
+        for bad in (dict(window=2.0, sinks=1), dict(window=2, sinks=1.0),
+                    dict(window=torch.tensor(2.0), sinks=1)):
+            with pytest.raises(TypeError):
+                _descriptor(b, **bad)
+        with pytest.raises(ValueError):
+            _descriptor(b, window=2 ** 31, sinks=1)
+        with pytest.raises((TypeError, ValueError)):
+            _descriptor(b, softmax_scale="wide")

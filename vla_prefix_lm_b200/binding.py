@@ -470,18 +470,20 @@ _paged_descs = {}
 def _paged_desc(B, Sq, Hq, dtype, k_pages, page_table, window=0, sinks=0, softmax_scale=1.0,
                 mask_stride=0):
     """(descriptor reference, workspace bytes) of a call."""
+    # Numbers only: a tensor would be looked up by its identity, whatever it holds by then.
+    window, sinks = operator.index(window), operator.index(sinks)
+    softmax_scale = float(softmax_scale)
     key = (B, Sq, Hq, dtype, k_pages.shape, k_pages.dtype, page_table.shape[1], window, sinks,
            softmax_scale, mask_stride, torch.cuda.current_device())
     got = _paged_descs.get(key)
     if got is None:
         n, page, Hkv, d = k_pages.shape
-        window, sinks = operator.index(window), operator.index(sinks)
         for x in (B, Sq, Hq, Hkv, n, page_table.shape[1], window, sinks):
             if not -2 ** 31 <= x < 2 ** 31:
                 raise ValueError(f"{x} does not fit the descriptor's 32 bits")
         desc = PiPagedDesc(B, Sq, Hq, Hkv, d, PI_BF16 if dtype == torch.bfloat16 else PI_F32,
                            _CACHE_CODES[k_pages.dtype], page, n, page_table.shape[1],
-                           window, sinks, float(softmax_scale), 0, mask_stride)
+                           window, sinks, softmax_scale, 0, mask_stride)
         ref = ctypes.byref(desc)
         got = (ref, int(lib().pi_attn_paged_workspace_bytes(ref)), desc)
         if len(_paged_descs) >= 1024:
