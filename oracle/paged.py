@@ -47,9 +47,11 @@ def exponent(vec: np.ndarray) -> int:
 
 
 def quantise(vec: np.ndarray):
-    """(e4m3 values, exponent byte) of one vector."""
+    """(e4m3 values, exponent byte) of one finite vector.  e = 120 is the largest
+    that 32-bit floats reach; 256 * 2^120 is out of their range: 240 is taken."""
     e = exponent(vec)
-    return to_e4m3(np.asarray(vec, np.float64) * 2.0 ** -e), e + 127
+    y = to_e4m3(np.asarray(vec, np.float64) * 2.0 ** -e)
+    return np.clip(y, -240, 240) if e == 120 else y, e + 127
 
 
 def positions(lens, S, mask=None):

@@ -12,7 +12,8 @@
 // lets the attention kernels rebuild bf16 operands without a second rounding.
 // Non-finite input: a NaN makes the whole vector NaN (byte 255, so that no
 // reader has to look for NaN bytes); an infinity reads back infinite (448 *
-// 2^120 overflows) and flushes the finite rest of its vector.
+// 2^120 overflows) and flushes the finite rest of its vector, up to 2^110.
+// Finite input reads back finite (cap_top).
 //
 // Both kernels move each byte once and are bound by HBM (long calls) or by
 // launch latency (a token per sequence).  d / 8 lanes own one vector, 8
@@ -111,6 +112,16 @@ __device__ __forceinline__ void store8(E4M3* p, const F8& f) {
 
 template <typename T> constexpr bool kIsE4M3 = false;
 template <> constexpr bool kIsE4M3<E4M3> = true;
+
+// The byte of e = 120, the largest that finite input takes (an infinity's too).
+constexpr uint32_t kTopByte = 247u;
+// Finite elements of a vector with that byte, scaled: from 248 on they would round
+// to 256, and 256 * 2^120 = 2^128 reads back infinite.  240 is within 2^-4 of them.
+__device__ __forceinline__ void cap_top(F8& f) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (fabsf(f.x[e]) <= 256.f) f.x[e] = fminf(fmaxf(f.x[e], -240.f), 240.f);
+}
 
 // The exponent byte of a vector whose largest magnitude has the bits u (above
 // infinity's: a NaN): 448 = 1.75 * 2^8, so 1.M * 2^(E - 127) needs e = E - 135, one
@@ -279,7 +290,9 @@ __global__ void __launch_bounds__(kCacheThreads)
         const uint32_t kb = exp_byte(ka), vb = exp_byte(va);
         // 2^-e = 2^(127 - byte): biased exponent 254 - byte, in [7, 253] (a NaN
         // vector: 0, what it holds does not matter)
-        const F8 kx = scaled(kr[i], 254u - min(kb, 254u)), vx = scaled(vr[i], 254u - min(vb, 254u));
+        F8 kx = scaled(kr[i], 254u - min(kb, 254u)), vx = scaled(vr[i], 254u - min(vb, 254u));
+        if (kb == kTopByte) cap_top(kx);
+        if (vb == kTopByte) cap_top(vx);
         if (slot >= 0) {
           store8(kp + dst * p.d + e0, kx);
           store8(vp + dst * p.d + e0, vx);
