@@ -50,3 +50,29 @@ def test_the_largest_finite_vectors_stay_finite(dtype):
         assert y[0, 4, 0, 0] == float("inf")
         assert y[0, 4, 0, 1] == 240 * 2.0 ** 120 and y[0, 4, 0, 2] == -240 * 2.0 ** 120
     assert b.pi_attn_read_status() == b.PI_OK
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("Sq,Hq,dtype", [(1, 8, BF16), (1, 1, BF16), (5, 1, BF16), (8, 1, BF16),
+                                         (4, 2, BF16), (40, 8, BF16), (150, 8, BF16), (9, 3, BF16),
+                                         (6, 2, F32)])
+@pytest.mark.parametrize("room", [0, 17000])
+def test_a_score_of_minus_infinity_has_no_weight(Sq, Hq, dtype, cache, room):
+    """Visible new keys whose scores are -inf, the first one among them, leave
+    the other keys' probabilities alone."""
+    if dtype == F32 and cache == BF16:
+        cache = F32
+    b = _b()
+    c = Cache(61, [40, 0, 300], 16, 1, 256, cache, room=room)
+    rng = c.rng
+    q = _rand(rng, (3, Sq, Hq, 256), dtype, 0.25)
+    kn, vn = (_rand(rng, (3, Sq, 1, 256), dtype, 0.25) for _ in range(2))
+    q[..., 7] = 1.0
+    kn[0, ::2, 0, 7] = float("-inf")
+    kn[2, ::3, 0, 7] = float("-inf")
+    if Sq > 2:                                     # (the query that sees itself alone is left)
+        kn[1, 2::3, 0, 7] = float("-inf")
+    ar = np.ones(Sq, np.uint8)
+    lse = torch.empty(q.shape[:3], device="cuda")
+    out = b.pi_attn_paged(q, kn, vn, *c.args(), torch.from_numpy(ar).cuda(), lse=lse, **c.exps())
+    _check(c, q, kn, vn, ar, None, out, lse, 1.0, 0, 0)

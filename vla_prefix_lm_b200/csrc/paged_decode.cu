@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
           for (int sh = 16; sh >= 1; sh >>= 1) sc += __shfl_xor_sync(0xffffffffu, sc, sh);
           sc *= sl2;
           const float mn = fmaxf(m[u], sc), f = m[u] == -INFINITY ? 0.f : ex2(m[u] - mn);
-          const float w = ex2(sc - mn);
+          const float w = sc == -INFINITY ? 0.f : ex2(sc - mn);     // (mn may be -inf too)
           l[u] = l[u] * f + w;
 #pragma unroll
           for (int c = 0; c < 8; ++c) acc[u][c] = fmaf(acc[u][c], f, w * v[c]);
