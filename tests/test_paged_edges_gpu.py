@@ -19,13 +19,14 @@ from test_paged_gpu import BF16, CACHES, E4M3, F32, Cache, _b, _check, _np, _ran
 pytestmark = pytest.mark.gpu
 
 
+@pytest.mark.parametrize("Hkv,d", [(1, 32), (3, 32), (1, 256), (2, 256)])
 @pytest.mark.parametrize("dtype", [F32, BF16])
-def test_the_largest_finite_vectors_stay_finite(dtype):
+def test_the_largest_finite_vectors_stay_finite(dtype, Hkv, d):
     """From 248 * 2^120 on, rounding to e4m3 would give 256 * 2^120 = 2^128,
     which no 32-bit float holds; such elements take 240 * 2^120, within 2^-4 of
     them, beside an infinity too."""
     b = _b()
-    c = Cache(60, [0], 16, 1, 32, E4M3, room=16)
+    c = Cache(60, [0], 16, Hkv, d, E4M3, room=16)
     top = torch.finfo(dtype).max
     x = torch.zeros(1, 6, 1, 32, dtype=torch.float64)
     x[0, 0, 0] = torch.linspace(-1, 1, 32, dtype=torch.float64) * top
@@ -34,21 +35,21 @@ def test_the_largest_finite_vectors_stay_finite(dtype):
     x[0, 3, 0, :3] = torch.tensor([247.0, 249.0, -255.0], dtype=torch.float64) * 2.0 ** 120
     x[0, 4, 0, :3] = torch.tensor([float("inf"), top, -top], dtype=torch.float64)
     x[0, 5, 0] = 2.0 ** 127
-    x = x.to(dtype).cuda()
+    x = x.to(dtype).repeat(1, 1, Hkv, d // 32).cuda()
+    x[0, 5, -1] = 1.0                              # heads of a token differ
     b.pi_attn_cache_write(x, x, *c.args(), **c.exps())
     c.lens += 6
     k, v, _ = b.pi_attn_cache_read(*c.args(), 6, dtype=dtype, **c.exps())
-    for y in (k, v):
-        for t in (0, 1, 2, 3, 5):
-            vals, byte = P.quantise(_np(x[0, t, 0]))
-            at = P.slot(c.table_np, 0, t, 16)
-            assert c.k_exp.view(-1)[at] == byte
-            assert np.array_equal(_np(y[0, t, 0]), vals * 2.0 ** (byte - 127)), t
-            err = np.abs(_np(y[0, t, 0]) - _np(x[0, t, 0]))
-            big = np.abs(_np(x[0, t, 0])) >= 2.0 ** -13 * np.abs(_np(x[0, t, 0])).max()
-            assert (err <= 2.0 ** -4 * np.abs(_np(x[0, t, 0])))[big].all(), t
-        assert y[0, 4, 0, 0] == float("inf")
-        assert y[0, 4, 0, 1] == 240 * 2.0 ** 120 and y[0, 4, 0, 2] == -240 * 2.0 ** 120
+    for y, exps in ((k, c.k_exp), (v, c.v_exp)):
+        for t, h in [(t, h) for t in (0, 1, 2, 3, 5) for h in range(Hkv)]:
+            x64, y64 = _np(x[0, t, h]), _np(y[0, t, h])
+            vals, byte = P.quantise(x64)
+            assert exps.view(-1, Hkv)[P.slot(c.table_np, 0, t, 16), h] == byte
+            assert np.array_equal(y64, vals * 2.0 ** (byte - 127)), (t, h)
+            err, big = np.abs(y64 - x64), np.abs(x64) >= 2.0 ** -13 * np.abs(x64).max()
+            assert (err <= 2.0 ** -4 * np.abs(x64))[big].all(), (t, h)
+        assert (y[0, 4, :, 0] == float("inf")).all()
+        assert (y[0, 4, :, 1] == 240 * 2.0 ** 120).all() and (y[0, 4, :, 2] == -240 * 2.0 ** 120).all()
     assert b.pi_attn_read_status() == b.PI_OK
 
 
