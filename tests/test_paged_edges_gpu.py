@@ -77,3 +77,39 @@ def test_a_score_of_minus_infinity_has_no_weight(Sq, Hq, dtype, cache, room):
     lse = torch.empty(q.shape[:3], device="cuda")
     out = b.pi_attn_paged(q, kn, vn, *c.args(), torch.from_numpy(ar).cuda(), lse=lse, **c.exps())
     _check(c, q, kn, vn, ar, None, out, lse, 1.0, 0, 0)
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("Sq,Hq,pads", [(3, 2, (1, 2, 0)), (7, 1, (3, 5, 6)), (8, 1, (7, 1, 2)),
+                                        (40, 8, (3, 39, 20)), (150, 8, (64, 30, 149)),
+                                        (300, 8, (33, 36, 250)), (700, 8, (1, 513, 200))])
+@pytest.mark.parametrize("window,sinks", [(37, 0), (37, 4), (200, 130)])
+@pytest.mark.parametrize("room", [0, 17000])
+def test_positions_hidden_from_all_but_padding_hold_nan(Sq, Hq, pads, window, sinks, cache, room):
+    """Padding in front: its tokens see nothing, so a cached position that lies in
+    the windows of padding alone is hidden, whatever it holds."""
+    b = _b()
+    lens = [200, 90, 333]
+    c = Cache(62, lens, 16, 1, 256, cache, room=room)
+    rng = c.rng
+    q = _rand(rng, (3, Sq, Hq, 256), BF16, 0.25)
+    kn, vn = (_rand(rng, (3, Sq, 1, 256), BF16, 0.25) for _ in range(2))
+    seg = np.zeros((3, Sq), np.int32)
+    live = np.zeros((c.k.shape[0], c.k.shape[1]), bool)
+    for i, (n, pad) in enumerate(zip(lens, pads)):
+        seg[i, :pad] = -1
+        first = min(max(0, n + pad - window + 1), n)         # the first real query sees the most
+        for x in list(range(min(sinks, n))) + list(range(first, n)):
+            live.reshape(-1)[P.slot(c.table_np, i, x, 16)] = True
+    dead = torch.from_numpy(~live).cuda()
+    for pool, exps in ((c.k, c.k_exp), (c.v, c.v_exp)):
+        if cache == E4M3:
+            exps[dead] = 255
+        else:
+            pool[dead] = float("nan")
+    ar = np.ones((3, Sq), np.uint8)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+    b.pi_attn_paged(q, kn, vn, *c.args(), torch.from_numpy(ar).cuda(),
+                    segment_ids=torch.from_numpy(seg).cuda(), out=out, lse=lse, window=window,
+                    sinks=sinks, **c.exps())
+    _check(c, q, kn, vn, ar, seg, out, lse, 1.0, window, sinks)

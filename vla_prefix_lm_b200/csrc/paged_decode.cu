@@ -478,6 +478,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     const uint32_t code0 = __shfl_sync(0xffffffffu, code, tk0);
     const uint32_t code1 = __shfl_sync(0xffffffffu, code, tk1);
     const bool row0_ok = qr0 < R && !is_pad(code0), row1_ok = qr1 < R && !is_pad(code1);
+    // No query sees a cached position before lo_live: padding in front sees nothing.
+    const uint32_t real = __ballot_sync(0xffffffffu, !is_pad(code));
+    const int lo_live =
+        p.window > 0 ? min(max(len + max(__ffs(real) - 1, 0) - p.window + 1, 0), len) : 0;
     const int lo_a = p.window > 0 ? min(max(len + tk0 - p.window + 1, 0), len) : 0;
     const int lo_b = p.window > 0 ? min(max(len + tk1 - p.window + 1, 0), len) : 0;
     // O^T [256 x 8 rows]: 16 column blocks of m16n8k16.
@@ -498,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                                                                        k0 + kTile <= p.sinks));
       if (!whole) {
         const int x = k0 + (lane & 15);
-        live = __ballot_sync(0xffffffffu, x < len && (p.window <= 0 || x >= sn.lo0 || x < p.sinks)) &
+        live = __ballot_sync(0xffffffffu, x < len && (p.window <= 0 || x >= lo_live || x < p.sinks)) &
                0xFFFFu;
       }
       if (!__all_sync(0xffffffffu, mbar_wait(&sm.k_full[warp], n_load & 1, ctl))) {

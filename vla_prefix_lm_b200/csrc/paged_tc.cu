@@ -97,7 +97,8 @@ struct Segment {
   int b, g, tile;            // sequence (absolute), kv head, query tile
   int tq0, tq1;              // its first / last new token
   int len;                   // cached tokens
-  int lo0, lo1;              // window start of the first / last token (cached positions)
+  int lo0, lo1;              // window start (cached positions) of the first token that is
+                             // not padding / of the last
   int sink_tiles, win_tile;  // cached tiles [0, sink_tiles) and [win_tile, ...)
   int n_cached, c0;          // number of cached tiles; first chunk tile
   int it0, n;                // this run: tiles [it0, it0 + n) of the unit's list
@@ -317,17 +318,19 @@ __device__ __forceinline__ void fill_segment(const PagedTcParams& p, const SmemT
   x.tq0 = x.tile * p.tok_per_tile;
   x.tq1 = min(x.tq0 + p.tok_per_tile, p.Sq) - 1;
   x.len = sm.plan.len[pl.b];
-  int any_e = 0, any_live = 0;
+  int any_e = 0;
+  uint32_t first = ~0u;                      // first token that is not padding
   for (int t = x.tq0 + lane; t <= x.tq1; t += 32) {
     const uint32_t c = codes[t];
     any_e |= (c >> 1) & 1;
-    any_live |= is_pad(c) ? 0 : 1;
+    if (!is_pad(c)) first = min(first, (uint32_t)t);
   }
   x.any_e = __any_sync(0xffffffffu, any_e);
-  const bool live = __any_sync(0xffffffffu, any_live);
+  first = __reduce_min_sync(0xffffffffu, first);
+  const bool live = first != ~0u;
   x.csq0 = codes[x.tq0] >> 2;
   x.csq1 = codes[x.tq1] >> 2;
-  x.lo0 = window_lo(p, x.len, x.tq0);
+  x.lo0 = window_lo(p, x.len, live ? (int)first : x.tq0);
   x.lo1 = window_lo(p, x.len, x.tq1);
   const int n_ct = (x.len + kBN - 1) / kBN;
   x.sink_tiles = p.window > 0 ? (min(p.sinks, x.lo0) + kBN - 1) / kBN : 0;
