@@ -113,3 +113,23 @@ def test_positions_hidden_from_all_but_padding_hold_nan(Sq, Hq, pads, window, si
                     segment_ids=torch.from_numpy(seg).cuda(), out=out, lse=lse, window=window,
                     sinks=sinks, **c.exps())
     _check(c, q, kn, vn, ar, seg, out, lse, 1.0, window, sinks)
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3, F32])
+def test_lengths_after_a_call_without_tokens(cache):
+    """Clamped and reported as in a call with tokens."""
+    b = _b()
+    c = Cache(63, [10, 20, 30], 16, 1, 64, cache)                # room for 32
+    empty = torch.empty(3, 0, 1, 64, dtype=F32 if cache == F32 else BF16, device="cuda")
+    before = [c.k.view(torch.uint8).clone(), c.v.view(torch.uint8).clone()]
+    got = torch.full((3,), -5, dtype=torch.int32, device="cuda")
+    b.pi_attn_cache_write(empty, empty, *c.args(), lens_out=got, **c.exps())
+    assert got.tolist() == [10, 20, 30] and b.pi_attn_read_status() == b.PI_OK
+    for bad, want in ((-7, 0), (33, 32), (2 ** 31 - 1, 32), (-2 ** 31, 0)):
+        lens = c.lens.clone()
+        lens[1] = bad
+        b.pi_attn_cache_write(empty, empty, c.k, c.v, c.table, lens, lens_out=got, **c.exps())
+        assert got.tolist() == [10, want, 30]
+        assert b.pi_attn_read_status() == b.PI_ERR_ARG
+    assert torch.equal(c.k.view(torch.uint8), before[0])
+    assert torch.equal(c.v.view(torch.uint8), before[1])

@@ -428,7 +428,8 @@ int tokens_per_cta(const CacheParams& p, int rows) {
 template <typename T, typename TC>
 cudaError_t launch(const CacheParams& p, bool write, const DevCtl& ctl, cudaStream_t st) {
   const int tok = tokens_per_cta(p, write ? kWriteRows : kReadRows);
-  dim3 grid((unsigned)((p.S + tok - 1) / tok), (unsigned)p.B);
+  // (Without tokens one CTA a sequence still writes its length.)
+  dim3 grid((unsigned)std::max((p.S + tok - 1) / tok, 1), (unsigned)p.B);
   return write ? launch_pdl(cache_write_kernel<T, TC>, grid, dim3(kCacheThreads), 0, st, p, ctl, tok)
                : launch_pdl(cache_read_kernel<T, TC>, grid, dim3(kCacheThreads), 0, st, p, ctl, tok);
 }

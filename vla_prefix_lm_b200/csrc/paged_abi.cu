@@ -133,12 +133,7 @@ int pi_attn_cache_write(const pi_paged_desc* d, const void* k_new, const void* v
   rc = check_cache(d, k_pages, v_pages, k_exp, v_exp, page_table, cache_lens);
   if (rc != PI_OK) return rc;
   if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(lens_out, 4)) return PI_ERR_ALIGN;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (d->Sq == 0) {
-    if (!lens_out) return PI_OK;
-    return launched(cudaMemcpyAsync(lens_out, cache_lens, sizeof(int32_t) * (size_t)d->B,
-                                    cudaMemcpyDeviceToDevice, st));
-  }
+  if (d->Sq == 0 && !lens_out) return PI_OK;
   DevCtl ctl;
   if (!make_ctl(&ctl)) return PI_ERR_CUDA;
   CacheParams p = cache_params(d);
@@ -147,7 +142,8 @@ int pi_attn_cache_write(const pi_paged_desc* d, const void* k_new, const void* v
   p.table = page_table; p.lens = cache_lens;
   p.tmask = token_mask; p.tmask_bs = d->mask_batch_stride;
   p.lens_out = lens_out;
-  return launched(launch_cache(p, true, d->dtype == PI_F32, d->cache_dtype, ctl, st));
+  return launched(launch_cache(p, true, d->dtype == PI_F32, d->cache_dtype, ctl,
+                               static_cast<cudaStream_t>(stream)));
 }
 
 int pi_attn_cache_read(const pi_paged_desc* d, const void* k_pages, const void* v_pages,
