@@ -133,3 +133,45 @@ def test_lengths_after_a_call_without_tokens(cache):
         assert b.pi_attn_read_status() == b.PI_ERR_ARG
     assert torch.equal(c.k.view(torch.uint8), before[0])
     assert torch.equal(c.v.view(torch.uint8), before[1])
+
+
+def test_long_chunks_from_several_threads():
+    """Calls of two lengths from four host threads: none is refused because
+    another thread prepares a shorter one.  (Padding throughout: only the
+    launches matter.)"""
+    b = _b()
+    L = b.lib()
+    c = Cache(64, [5], 16, 1, 32, F32)
+    jobs = []
+    for Sq in (16383, 8300):
+        q = torch.zeros(1, Sq, 1, 32, device="cuda")
+        out = torch.full_like(q, 3.0)
+        ar = torch.ones(Sq, dtype=torch.uint8, device="cuda")
+        seg = torch.full((Sq,), -1, dtype=torch.int32, device="cuda")
+        d = b.PiPagedDesc(1, Sq, 1, 1, 32, b.PI_F32, b.PI_F32, 16, c.k.shape[0], c.table.shape[1],
+                          0, 0, 1.0, 0, 0)
+        assert L.pi_attn_paged_workspace_bytes(ctypes.byref(d)) == 0
+        p = [t.data_ptr() for t in (q, q, q, ar, seg, c.k, c.v)]
+        args = (ctypes.byref(d), *p, None, None, c.table.data_ptr(), c.lens.data_ptr(),
+                out.data_ptr(), None, None, 0, None)
+        jobs.append(((q, ar, seg, out), args))
+    bad = []
+
+    def run(i):
+        args = jobs[i % 2][-1]
+        for _ in range(600):
+            rc = L.pi_attn_paged(*args)
+            if rc != b.PI_OK:
+                bad.append((i % 2, rc))
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not bad, (len(bad), bad[:3])
+    for tensors, _ in jobs:
+        assert (tensors[-1] == 0).all()
+    assert b.pi_attn_read_status() == b.PI_OK

@@ -250,9 +250,11 @@ template <int D, typename T, typename TC, bool kSplit>
 cudaError_t launch_as(const PagedParams& p, const DevCtl& ctl, cudaStream_t st) {
   const size_t smem = sizeof(uint32_t) * (size_t)p.Sq;
   if (smem > 32 * 1024) {                    // (what else the kernel has is under 16 KB)
+    // The bound of every call, not this one's size: another thread's shorter chunk
+    // would lower it before this launch.
     const cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<D, T, TC, kSplit>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem);
+                                               (int)sizeof(uint32_t) * kMaxTokens);
     if (e != cudaSuccess) return e;
   }
   const int n = kSplit ? p.Sq * p.Hq : (p.Sq + kTokens - 1) / kTokens;
