@@ -121,6 +121,12 @@ __global__ void selftest_wait_kernel(DevCtl ctl) {
   __syncthreads();
 }
 
+// Codes up to here need no larger limit (48 KB hold them and what the kernels have of
+// their own).  Above, the limit is that of the longest call: it belongs to the kernel,
+// so that another thread's shorter call must not lower it before a launch.
+constexpr size_t kPlainSmem = 47 * 1024;
+constexpr int kMaxCodeBytes = (int)sizeof(uint32_t) * kMaxTokens;
+
 }  // namespace
 
 cudaError_t launch_simt_f32(const SimtParams& p, const DevCtl& ctl, cudaStream_t st) {
@@ -128,9 +134,9 @@ cudaError_t launch_simt_f32(const SimtParams& p, const DevCtl& ctl, cudaStream_t
   dim3 grid((p.Sq + kSimtTokensPerBlock - 1) / kSimtTokensPerBlock, p.B);
   const size_t smem = sizeof(uint32_t) * (size_t)p.Sq;
   auto launch = [&](auto kern) -> cudaError_t {
-    if (smem > 48 * 1024) {
+    if (smem > kPlainSmem) {
       cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)smem);
+                                           kMaxCodeBytes);
       if (e != cudaSuccess) return e;
     }
     kern<<<grid, kSimtThreads, smem, st>>>(p);
@@ -150,9 +156,9 @@ cudaError_t launch_debug_mask(int mode, int B, int Sq, int P, const uint8_t* ar,
                               cudaStream_t st) {
   dim3 grid((Sq + 7) / 8, B);
   const size_t smem = sizeof(uint32_t) * (size_t)Sq;
-  if (smem > 48 * 1024) {
+  if (smem > kPlainSmem) {
     cudaError_t e = cudaFuncSetAttribute(debug_mask_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxCodeBytes);
     if (e != cudaSuccess) return e;
   }
   debug_mask_kernel<<<grid, 256, smem, st>>>(mode, Sq, P, ar, seg, mask_bs, out);
