@@ -363,13 +363,14 @@ size_t pi_attn_suffix_noalloc_capacity(void);
  *   cache_lens       [B] int32: tokens already cached
  *
  * Quantisation (PI_E4M3): a vector's scale is the smallest power of two, at
- * least 2^-126, that brings its largest magnitude to at most 448; its elements
- * are rounded to nearest even once, at most 2^-4 of their value (down to
- * 2^-14 of the largest; below that 2^-10 of the scale), and the scale is undone
+ * least 2^-126, that brings its largest magnitude to at most 448 (1 for a zero
+ * vector); its elements are rounded to nearest even once, by at most the larger of
+ * 2^-4 of their value and 2^-10 of the scale (the former, unless the scale is 2^-126,
+ * for all elements from 2^-13 of the largest on), and the scale is undone
  * exactly.  (Elements from 248 * 2^120 on take 240 * 2^120: finite input reads
  * back finite.)  A vector holding a NaN reads back as NaN (exponent byte 255); one
  * holding an infinity reads back infinite there and flushes its finite elements
- * up to 2^110.
+ * up to 2^110.  (Attention may take cached values below 2^-126 for zero.)
  * The e4m3 byte 0x7F (NaN) is not part of the format.
  *
  * Lengths, tables and masks are device data: a length outside [0, max_pages *

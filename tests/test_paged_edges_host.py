@@ -13,6 +13,7 @@ import pytest
 import torch
 
 from conftest import ROOT
+from oracle import paged as P
 from test_paged_host import _attend, _desc, _lib
 
 
@@ -126,3 +127,40 @@ def test_refusals_do_not_depend_on_earlier_calls(monkeypatch):
             _descriptor(b, window=2 ** 31, sinks=1)
         with pytest.raises((TypeError, ValueError)):
             _descriptor(b, softmax_scale="wide")
+
+
+# ------------------------------------------------------ the stated rounding bounds
+
+@pytest.mark.parametrize("top", [224.0001, 225.0, 256.0, 300.0, 447.9, 448.0])
+@pytest.mark.parametrize("e", [-125, -126, -20, 0, 17, 119, 120])
+def test_the_headers_rounding_bounds(top, e):
+    """The larger of 2^-4 of the value (half a step of 2^-3 * 2^k for scaled values in
+    [2^k, 2^(k+1)), k >= -6) and 2^-10 of the scale (half of the subnormals' step,
+    2^-9); 224 * 2^-13 > 2^-6, so the former from 2^-13 of the largest on."""
+    if top * 2.0 ** e >= 2.0 ** 128:
+        pytest.skip("past the largest float")
+    x = np.concatenate([[top], top * np.exp2(np.linspace(-16, 0, 20001))]) * 2.0 ** e
+    vals, byte = P.quantise(x)
+    assert byte == e + 127
+    err, scale = np.abs(vals * 2.0 ** e - x), 2.0 ** e
+    near = x >= 2.0 ** -13 * x[0]
+    assert (err[near] <= 2.0 ** -4 * x[near]).all()
+    assert (err <= np.maximum(2.0 ** -4 * x, 2.0 ** -10 * scale)).all()
+    if top < 230:                      # and not from 2^-14 on: e4m3 is subnormal there
+        far = x >= 2.0 ** -14 * x[0]
+        assert (err[far] > 2.0 ** -4 * x[far]).any()
+
+
+@pytest.mark.parametrize("top", [1e-44, 1e-40, 1.1754943508222875e-38, 1e-36])
+def test_the_bounds_where_the_exponent_stops(top):
+    x = top * np.linspace(0, 1, 1001)
+    vals, byte = P.quantise(x)
+    assert byte == 1
+    scale = 2.0 ** -126
+    err = np.abs(vals * scale - x)
+    assert (err <= np.maximum(2.0 ** -4 * x, 2.0 ** -10 * scale)).all()
+
+
+def test_a_zero_vector_has_scale_one():
+    vals, byte = P.quantise(np.zeros(4))
+    assert byte == 127 and (vals == 0).all()

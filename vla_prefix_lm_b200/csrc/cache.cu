@@ -7,8 +7,9 @@
 // as y = rn_e4m3(x * 2^-e) with e the smallest integer for which amax(|x|) <=
 // 448 * 2^e (e >= -126), byte = e + 127.  A power of two costs nothing: e4m3
 // keeps its 3 mantissa bits over 2^-6 .. 448 wherever amax falls in (224, 448],
-// so every element down to amax * 2^-14 is rounded once, by at most half a
-// step (2^-4 of it), and undoing the scale is exact in bf16 and fp32, which
+// so every element down to amax * 2^-13 is rounded once, by at most half a
+// step (2^-4 of it; 2^-10 of the scale where e4m3 is subnormal, also for larger
+// elements if e stops at -126), and undoing the scale is exact in bf16 and fp32, which
 // lets the attention kernels rebuild bf16 operands without a second rounding.
 // Non-finite input: a NaN makes the whole vector NaN (byte 255, so that no
 // reader has to look for NaN bytes); an infinity reads back infinite (448 *
