@@ -164,3 +164,28 @@ def test_the_bounds_where_the_exponent_stops(top):
 def test_a_zero_vector_has_scale_one():
     vals, byte = P.quantise(np.zeros(4))
     assert byte == 127 and (vals == 0).all()
+
+
+# ------------------------------------------------------------------ a C client
+
+def test_plain_c_client_and_the_descriptors_layout(tmp_path):
+    b, _ = _lib()
+    gcc = shutil.which("gcc")
+    if gcc is None:
+        pytest.skip("no C compiler")
+    exe, libdir = tmp_path / "paged_check", os.path.join(ROOT, "vla_prefix_lm_b200")
+    subprocess.run([gcc, "-std=c11", "-Wall", "-Wextra", "-Werror",
+                    "-I", os.path.join(ROOT, "include"),
+                    os.path.join(ROOT, "tests", "c_abi", "paged_check.c"),
+                    "-L", libdir, "-lpiattn", f"-Wl,-rpath,{libdir}", "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0, r.stderr
+    lines = r.stdout.split("\n")
+    assert "c abi ok" in lines
+    got = {w[0]: tuple(map(int, w[1:])) for w in map(str.split, lines) if len(w) == 3 and w[0] != "c"}
+    want = {}
+    for name, _ in b.PiPagedDesc._fields_:
+        field = getattr(b.PiPagedDesc, name)
+        want[name] = (field.offset, field.size)
+    assert got == want
+    assert f"size {ctypes.sizeof(b.PiPagedDesc)}" in lines
