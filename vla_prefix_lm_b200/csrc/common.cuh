@@ -339,6 +339,11 @@ __device__ __forceinline__ void cluster_sync() {
                ::: "memory");
 }
 
+// A 32-bit store to a shared::cluster address.
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // Arrive on an mbarrier given by a shared::cluster address (possibly the
 // peer CTA's), with the default release semantics.  A cluster-scope release
 // here costs ~1000 cycles per arrival; the data this signal publishes (TMEM

@@ -185,6 +185,15 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int* abor
   return true;
 }
 
+// After a wait ran out in either CTA, when neither starts anything more.  A loader
+// that was ahead of its partner has copies under way whose barrier, in the even CTA,
+// lacks the partner's arrivals and never completes: no wait covers them.  They come
+// from this GPU's own memory, within microseconds; this is about half a millisecond.
+__device__ __noinline__ void settle() {
+  const long long t0 = clock64();
+  while (clock64() - t0 < (1ll << 20)) __nanosleep(1000);
+}
+
 // Warp-uniform bounded wait: every lane polls, all get the same answer.
 template <class SmemT>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, SmemT& sm,
@@ -1373,7 +1382,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && sm.abort) st_cluster_u32(mapa_shared(smem_u32(&sm.abort), rank ^ 1u), 1u);
   cluster_sync();
+  if (sm.abort) settle();
   if (warp == 12) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
