@@ -5,7 +5,7 @@
 // G query heads of one key/value head, 128 rows per CTA, against tiles of 128
 // keys (cached tiles first, then the chunk's own).  Per key tile
 //   S = Q K^T   tcgen05.mma.cta_group::2, M = 256: K split by keys (64 per CTA)
-//   P           fp32 online softmax, one thread per row, P rounded to bf16 once
+//   P           fp32 online softmax, two threads per row, P rounded to bf16 once
 //   O += P V    tcgen05.mma.cta_group::2: V split by columns (128 per CTA)
 // as in the dense kernel (tc_pair.cu).  What differs is how keys arrive and how
 // the work is shared out.
@@ -119,6 +119,8 @@ struct Layout {
   static constexpr int kOffCtl = kOffP + kPBytes;
 };
 constexpr int kTiles = (kMaxTokens + kBN - 1) / kBN;
+// What a chunk tile holds (tile_fast; a padding token is FAST too).
+constexpr uint32_t kTileFast = 1u, kTilePad = 2u;
 // Codes of longer chunks live in the workspace (one copy per CTA).
 constexpr int kSmemTokens = 512;
 
@@ -394,7 +396,7 @@ __device__ __forceinline__ void scan_codes(const PagedTcParams& p, SmemT& sm, ui
       on[i] = t < p.Sq ? ar[t] : 0u;
       sg[i] = t < p.Sq && seg ? seg[t] : 0;
     }
-    uint32_t any_f = 0, all_f = ~0u, any_p = 0, all_p = ~0u;
+    uint32_t any_f = 0, any_p = 0;
     uint32_t first = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -409,15 +411,12 @@ __device__ __forceinline__ void scan_codes(const PagedTcParams& p, SmemT& sm, ui
       const uint32_t f = __ballot_sync(0xffffffffu, (code & 1u) != 0u) & live;
       const uint32_t q = __ballot_sync(0xffffffffu, is_pad(code)) & live;
       any_f |= f;
-      all_f &= f | ~live;
       any_p |= q;
-      all_p &= q | ~live;
     }
     if (lane == 0) {
       sm.tile_cs_first[t0 / kBN] = (uint16_t)first;
       sm.tile_cs_last[t0 / kBN] = (uint16_t)cs;
-      sm.tile_fast[t0 / kBN] = (uint8_t)((any_f ? 1u : 0u) | (all_f == ~0u ? 2u : 0u) |
-                                         (any_p ? 4u : 0u) | (all_p == ~0u ? 8u : 0u));
+      sm.tile_fast[t0 / kBN] = (uint8_t)((any_f ? kTileFast : 0u) | (any_p ? kTilePad : 0u));
     }
   }
   __syncwarp();
@@ -1168,8 +1167,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool partial;
         if (kt.chunk) {
           const uint32_t fl = sm.tile_fast[kt.tile];
-          partial = k0 + kBN > p.Sq || sm.tile_cs_last[kt.tile] > x.csq0 || (fl & 4u) ||
-                    (x.any_e && (fl & 1u)) ||
+          partial = k0 + kBN > p.Sq || sm.tile_cs_last[kt.tile] > x.csq0 || (fl & kTilePad) ||
+                    (x.any_e && (fl & kTileFast)) ||
                     (p.window > 0 && x.tq1 - k0 >= p.window && x.len + k0 + kBN > p.sinks);
         } else {
           partial = k0 + kBN > x.len || (p.window > 0 && k0 < x.lo1 && k0 + kBN > p.sinks);
