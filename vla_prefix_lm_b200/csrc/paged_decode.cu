@@ -916,17 +916,26 @@ cudaError_t launch(const PagedDecodeParams& p, const DevCtl& ctl, cudaStream_t s
 
 // Whether a cluster takes each unit: all clusters are resident at once, and the
 // longest cache that the page table can hold is neither too long for eight CTAs nor,
-// with few units, worth spreading over more.  Measured, split in two launches / a
-// cluster each, bf16, lengths from half to all of the stated one: 1 sequence of 880
-// 10.4 / 8.3 us, 4000 12.3 / 11.7, 8000 14.3 / 15.3; 4 of 8000 22.6 / 20.5; 16 of 880
-// 13.0 / 9.5, 8000 30 / 25; 32 of 880 14.7 / 11.5, 8000 43 / 39; 64 of 880 19.7 / 22.7,
-// 128 of 880 27 / 34.
+// with few units, worth spreading over more.  An e4m3 tile is half the bytes of a bf16
+// one and more instructions, so that eight CTAs are the limit sooner.  Measured, split
+// in two launches / a cluster each, us, lengths from half to all of the stated one:
+//   bf16, 1 sequence of 880 10.4 / 8.3, 4000 12.3 / 11.7, 8000 16.4 / 17.8; 2 of 12000
+//   24.5 / 22.3; 4 of 8000 23.6 / 18.9, 12000 25.5 / 23.5, 14000 24.5 / 27.4; 8 of 12000
+//   28.5 / 28.0, 16000 33.1 / 35.5; 12 of 16000 39.4 / 37.6; 16 of 880 13.0 / 9.5, 16000
+//   45.3 / 42.0, 32000 72.8 / 75.7; 32 of 880 14.7 / 11.5, 16000 71.4 / 70.5; 55 of 2000
+//   26.0 / 27.6; 64 of 880 19.7 / 22.7, 128 of 880 27 / 34.
+//   e4m3, 1 of 880 10.5 / 8.6, 2000 11.3 / 11.0, 3000 12.3 / 12.6; 2 of 3000 13.6 / 13.4,
+//   6000 17.0 / 19.6; 4 of 5000 20.4 / 18.2, 8000 23.6 / 24.8; 16 of 3000 19.2 / 15.4, 5000
+//   21.9 / 22.4, 16000 36.6 / 56.4; 32 of 880 15.3 / 11.5, 5000 27.0 / 26.7, 16000 52.5 /
+//   68.2; 44 of 4000 28.1 / 24.2; 55 of 1500 20.2 / 22.9.
 bool clustered(const PagedParams& p) {
   const long long units = (long long)p.B * p.Hkv;
   long long n = (long long)p.max_pages << p.page_shift;
   if (p.window > 0) n = min(n, (long long)p.window + p.sinks);
-  return units * kClusterCtas <= (long long)sm_count() * kPerSm &&
-         n <= min(5000 * units, 16384ll);
+  const long long longest = p.cache_dtype == kCacheE4M3
+                                ? min(2000 * units, 5120ll)
+                                : min(5000 * units, units < 12 ? 12288ll : 16384ll);
+  return units * kClusterCtas <= (long long)sm_count() * kPerSm && n <= longest;
 }
 
 }  // namespace
