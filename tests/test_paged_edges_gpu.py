@@ -175,3 +175,71 @@ def test_long_chunks_from_several_threads():
     for tensors, _ in jobs:
         assert (tensors[-1] == 0).all()
     assert b.pi_attn_read_status() == b.PI_OK
+
+
+def _at(t, shift):
+    """t's values at an address `shift` bytes past a multiple of 256."""
+    raw = torch.full((t.numel() * t.element_size() + 512,), 0x7F, dtype=torch.uint8, device="cuda")
+    raw = raw[shift:shift + t.numel() * t.element_size()]
+    assert raw.data_ptr() % 256 == shift
+    raw.copy_(t.contiguous().view(torch.uint8).view(-1))
+    return raw.view(t.dtype).view(t.shape)
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("Sq,Hq", [(1, 8), (6, 1), (51, 8), (130, 8), (520, 8), (9, 3)])
+def test_the_least_alignment_that_is_asked_for(Sq, Hq, cache):
+    """Tensors, pools and workspace at 16 bytes, int32 and fp32 arrays at 4, masks
+    and exponents at odd addresses: the same bits as with aligned ones."""
+    b = _b()
+    c = Cache(65, [333, 0, 1200], 32, 1, 256, cache, room=Sq)
+    q = _rand(c.rng, (3, Sq, Hq, 256), BF16, 0.25)
+    kn, vn = (_rand(c.rng, (3, Sq, 1, 256), BF16, 0.25) for _ in range(2))
+    ar = torch.from_numpy((c.rng.random((3, Sq)) < 0.3).astype(np.uint8)).cuda()
+    seg = torch.from_numpy(c.rng.integers(-1, 3, (3, Sq)).astype(np.int32)).cuda()
+    mask = torch.from_numpy((c.rng.random((3, Sq)) < 0.7).astype(np.uint8)).cuda()
+
+    def step(move):
+        q_, kn_, vn_, k, v = (move(t, 16 * (i + 1)) for i, t in enumerate((q, kn, vn, c.k, c.v)))
+        table, lens, sg = (move(t, 4 * (i + 1)) for i, t in enumerate((c.table, c.lens, seg)))
+        ar_, mask_ = move(ar, 1), move(mask, 7)
+        exps = {n: move(e, 3) for n, e in c.exps().items() if e is not None}
+        out, lse = move(torch.zeros_like(q), 48), move(torch.zeros(q.shape[:3], device="cuda"), 12)
+        after = move(torch.zeros_like(c.lens), 4)
+        need = b.pi_attn_paged_workspace_bytes(q_, kn_, k, v, table, lens, **exps)
+        ws = move(torch.zeros(max(need, 16), dtype=torch.uint8, device="cuda"), 16)
+        b.pi_attn_paged(q_, kn_, vn_, k, v, table, lens, ar_, segment_ids=sg, out=out, lse=lse,
+                        workspace=ws, **exps)
+        b.pi_attn_cache_write(kn_, vn_, k, v, table, lens, token_mask=mask_, lens_out=after, **exps)
+        n = int(after.max())
+        ko, vo = (move(torch.zeros(3, n, 1, 256, dtype=BF16, device="cuda"), 80) for _ in range(2))
+        valid = move(torch.zeros(3, n, dtype=torch.uint8, device="cuda"), 5)
+        b.pi_attn_cache_read(k, v, table, after, n, k_out=ko, v_out=vo, valid_out=valid, **exps)
+        assert b.pi_attn_read_status() == b.PI_OK
+        return [t.contiguous().view(torch.uint8) for t in (out, lse, after, k, v, ko, vo, valid,
+                                                           *exps.values())]
+
+    for x, y in zip(step(_at), step(lambda t, shift: t.clone())):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("cache", CACHES)
+def test_streams_as_objects_and_handles(cache):
+    """stream= takes a torch stream or its handle; results of all calls agree."""
+    b = _b()
+    c = Cache(66, [300, 40], 16, 1, 256, cache, room=60)
+    for Sq in (1, 40):
+        q = _rand(c.rng, (2, Sq, 8, 256), BF16, 0.25)
+        kn, vn = (_rand(c.rng, (2, Sq, 1, 256), BF16, 0.25) for _ in range(2))
+        ar = torch.ones(Sq, dtype=torch.uint8, device="cuda")
+        ref = b.pi_attn_paged(q, kn, vn, *c.args(), ar, **c.exps())
+        rows = b.pi_attn_cache_read(*c.args(), 50, **c.exps())
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        for stream in (side, side.cuda_stream, torch.cuda.current_stream(), 0):
+            out = b.pi_attn_paged(q, kn, vn, *c.args(), ar, stream=stream, **c.exps())
+            got = b.pi_attn_cache_read(*c.args(), 50, stream=stream, **c.exps())
+            torch.cuda.synchronize()
+            assert torch.equal(out, ref)
+            assert all(torch.equal(x, y) for x, y in zip(got, rows))
+    assert b.pi_attn_read_status() == b.PI_OK
