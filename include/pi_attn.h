@@ -422,7 +422,8 @@ int pi_attn_cache_write(const pi_paged_desc* desc, const void* k_new, const void
  *   k_out, v_out [B, Sq, Hkv, d] dtype: the cached vectors (rounded to dtype
  *                once); rows past a sequence's length are zeros
  *   valid_out    [B, Sq] uint8 or NULL: 1 for a cached row, 0 past the length
- * desc: as pi_attn_cache_write; mask_batch_stride is not read; any Sq.
+ * desc: as pi_attn_cache_write; mask_batch_stride is not read; Sq below
+ * 2^31 - 2^15.
  */
 int pi_attn_cache_read(const pi_paged_desc* desc, const void* k_pages, const void* v_pages,
                        const uint8_t* k_exp, const uint8_t* v_exp, const int32_t* page_table,

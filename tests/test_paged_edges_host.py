@@ -14,7 +14,7 @@ import torch
 
 from conftest import ROOT
 from oracle import paged as P
-from test_paged_host import _attend, _desc, _lib
+from test_paged_host import _attend, _desc, _lib, _read, _write
 
 
 def test_rows_that_a_loop_of_32_bits_cannot_count_are_refused():
@@ -25,6 +25,15 @@ def test_rows_that_a_loop_of_32_bits_cannot_count_are_refused():
         d = _desc(b, B=1, Sq=Sq, Hq=Hq, d=32)
         assert L.pi_attn_paged_workspace_bytes(ctypes.byref(d)) == 0
         assert _attend(L, d) == b.PI_ERR_UNSUPPORTED
+
+
+def test_rows_to_read_past_32_bits_are_refused():
+    """From 2^31 - 2^15 on, rounding Sq up to whole CTAs would wrap."""
+    b, L = _lib()
+    for Sq in ((1 << 31) - 1, (1 << 31) - (1 << 15)):
+        assert _read(L, _desc(b, Sq=Sq)) == b.PI_ERR_UNSUPPORTED
+        assert _write(L, _desc(b, Sq=Sq)) == b.PI_ERR_UNSUPPORTED
+        assert _attend(L, _desc(b, Sq=Sq)) == b.PI_ERR_UNSUPPORTED
 
 
 STAGE_CHECK = r"""

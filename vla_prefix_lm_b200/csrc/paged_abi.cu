@@ -46,7 +46,7 @@ int check_desc(const pi_paged_desc* d) {
     return PI_ERR_UNSUPPORTED;
   constexpr long long kMaxSlots = (1ll << 31) - (1ll << 15);
   if ((long long)d->num_pages * d->page_size >= kMaxSlots ||
-      (long long)d->max_pages * d->page_size >= kMaxSlots)
+      (long long)d->max_pages * d->page_size >= kMaxSlots || d->Sq >= kMaxSlots)
     return PI_ERR_UNSUPPORTED;
   if (d->B > 65535 || d->Hkv > 65535) return PI_ERR_UNSUPPORTED;
   return PI_OK;
