@@ -448,6 +448,8 @@ int pi_attn_cache_read(const pi_paged_desc* desc, const void* k_pages, const voi
  * x < sinks; new key j stands at position cache_lens[b] + j (padding tokens
  * count, so the positions are the stored ones when padding is on the right).
  * window == 0: no limit (sinks is not read).
+ * Scores are sums in fp32; a cached vector's power-of-two scale may be applied to the
+ * sum, so that they need |softmax_scale * q| below 2^100 over an 8-bit cache.
  * A row that sees no key writes out = 0, lse = -inf.  What masked or stale
  * slots hold (NaN included) does not reach the result, except that a
  * non-finite value vector seen by some query of a sequence may make the

@@ -23,7 +23,7 @@
 // keeps the loads of several vectors of keys and of values in flight.  Measured: 32
 // prefixes of 824 tokens to e4m3 in 11.5 us (3.5 TB/s; 20 us with the loads behind
 // the slot lookups and the scaling in fp32), four bf16 sequences of up to 16000
-// tokens read back in 17.2 us (6.7 TB/s), a token for each of 32 sequences 2.4 us.
+// tokens read back in 17.2 us (6.7 TB/s), a token for each of 32 sequences 2.2 us.
 #include <algorithm>
 
 #include "launch.h"
