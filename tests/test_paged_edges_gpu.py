@@ -243,3 +243,37 @@ def test_streams_as_objects_and_handles(cache):
             assert torch.equal(out, ref)
             assert all(torch.equal(x, y) for x, y in zip(got, rows))
     assert b.pi_attn_read_status() == b.PI_OK
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("Sq,Hq,d,dtype", [(1, 8, 256, BF16), (4, 2, 256, BF16), (40, 8, 256, BF16),
+                                           (150, 8, 256, BF16), (9, 3, 256, BF16), (9, 4, 64, BF16),
+                                           (9, 4, 64, F32)])
+@pytest.mark.parametrize("room", [0, 17000])
+def test_a_nan_query_stays_in_its_row(Sq, Hq, d, dtype, cache, room):
+    """NaN and infinite queries turn their own row and lse to NaN, and no bit of
+    another row changes."""
+    if dtype == F32 and cache == BF16:
+        cache = F32
+    b = _b()
+    c = Cache(67, [900, 7, 2100], 64, 1, d, cache, room=room)
+    q = _rand(c.rng, (3, Sq, Hq, d), dtype, 0.25)
+    kn, vn = (_rand(c.rng, (3, Sq, 1, d), dtype, 0.25) for _ in range(2))
+    ar = torch.ones(Sq, dtype=torch.uint8, device="cuda")
+
+    def call(q):
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+        b.pi_attn_paged(q, kn, vn, *c.args(), ar, out=out, lse=lse, **c.exps())
+        assert b.pi_attn_read_status() == b.PI_OK
+        return out, lse
+
+    ref, ref_lse = call(q)
+    bad = q.clone()
+    hit = torch.zeros(q.shape[:3], dtype=torch.bool, device="cuda")
+    for i, x in ((0, "nan"), (2, "inf")):
+        t, h = Sq // 2, i % Hq
+        bad[i, t, h, 5] = float(x)
+        hit[i, t, h] = True
+    out, lse = call(bad)
+    assert torch.equal(out[~hit], ref[~hit]) and torch.equal(lse[~hit], ref_lse[~hit])
+    assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
